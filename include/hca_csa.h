@@ -67,7 +67,7 @@ typedef enum {
 
 typedef enum { HCSA_F32 = 0, HCSA_BF16 = 1 } hcsa_dtype;
 
-typedef enum { HCSA_KIND_CSA = 0, HCSA_KIND_HCA = 1 } hcsa_kind;
+typedef enum { HCSA_KIND_CSA = 0, HCSA_KIND_HCA = 1, HCSA_KIND_SWA = 2 } hcsa_kind;
 
 /* One struct describes a layer; each call reads the fields it needs. */
 typedef struct {
@@ -119,6 +119,17 @@ typedef struct {
      * entries [0, n_cap) and ent0 must be 0. */
     int32_t ent0;
     int32_t ent_shard;
+    /* Sliding-window layers (the swa_* calls; no other call reads these fields, so a caller built against
+     * the struct without them keeps working).  H query heads share Hkv key / value heads in groups of
+     * H / Hkv (query head h reads key head h / (H / Hkv)); C = 2 dh (the key and value of one head),
+     * m = width = 1; window is the number of recent tokens a query sees, itself included (INT32_MAX: all),
+     * and the first `sinks` tokens of the sequence stay visible.  The paged cache has n_pages pages of
+     * `page` tokens (a multiple of 16); a sequence has at most max_pages of them. */
+    int32_t Hkv;
+    int32_t sinks;
+    int32_t page;
+    int32_t n_pages;
+    int32_t max_pages;
 } hcsa_params;
 
 /* Decode cache of one layer (device pointers, caller-owned).
@@ -137,6 +148,19 @@ typedef struct {
     void *ring_ki;
 } hcsa_cache;
 
+/* Paged key / value cache of one sliding-window layer (device pointers, caller-owned).
+ * k_pages, v_pages [n_pages, Hkv, page, dh]  token p of sequence b, head g at page
+ *                  page_table[b, p / page], row p % page.  Storage as p->dtype, or with p->lowprec = 1
+ *                  (bf16 layers, dh a multiple of 32) the FP8 layout of hcsa_params.lowprec over the
+ *                  n_pages * Hkv * page rows of dh channels: all codes, then all int8 exponents
+ *                  (hcsa_page_bytes gives the size)
+ * page_table       [B, max_pages] int32; entries past a sequence's last page are not read */
+typedef struct {
+    void *k_pages;
+    void *v_pages;
+    const int32_t *page_table;
+} hcsa_pages;
+
 /* Workspace queries: op selects the call. */
 typedef enum {
     HCSA_OP_PROJECT = 0,
@@ -148,7 +172,8 @@ typedef enum {
     HCSA_OP_HCA_DECODE_ATTEND = 6,
     HCSA_OP_CSA_DECODE_INDEX_TOPK_SHARD = 7,
     HCSA_OP_CSA_DECODE_ATTEND_SHARD = 8,
-    HCSA_OP_HCA_DECODE_ATTEND_SHARD = 9
+    HCSA_OP_HCA_DECODE_ATTEND_SHARD = 9,
+    HCSA_OP_SWA_DECODE_ATTEND = 10
 } hcsa_op;
 
 /* Library version (major * 10000 + minor * 100 + patch). */
@@ -161,7 +186,8 @@ const char *hcsa_status_string(hcsa_status s);
 size_t hcsa_workspace_bytes(const hcsa_params *p, int32_t op);
 
 /* Number of projected columns for a layer of `kind`:
- * CSA: C (kv) + C (g) + di (ki) + Hi*di (qi) + Hi (w) + H*dh (q);  HCA: C + C + H*dh. */
+ * CSA: C (kv) + C (g) + di (ki) + Hi*di (qi) + Hi (w) + H*dh (q);  HCA: C + C + H*dh;
+ * SWA: Hkv*dh (k) + Hkv*dh (v) + H*dh (q). */
 int64_t hcsa_proj_cols(const hcsa_params *p, int32_t kind);
 
 /* Bytes of an entries array (hcsa_entry_bytes) or an indexer-key array (hcsa_key_bytes) of `rows`
@@ -354,6 +380,65 @@ hcsa_status hcsa_merge_partials(const hcsa_params *p, const float *parts, int32_
 hcsa_status csa_decode_index_topk_noalloc(const hcsa_params *p, const hcsa_cache *cache, const int32_t *pos,
                                           const void *qi, int64_t ld_qi, const void *w, int64_t ld_w,
                                           int32_t *sel, void *stream);
+
+/* ---- sliding-window layers: uncompressed attention over the recent window and the first tokens, the
+ * layers that a hybrid stack mixes with its compressed ones (section "Ventana deslizante: el contexto
+ * reciente conserva detalle", and the sliding-window block that ends the schedule of "Pila hibrida de
+ * capas").  The pages give no formula; the operator is
+ *     out[t, h] = sum_j softmax_j(scale q[t, h] . k[j, g]) v[j, g],   g = h / (H / Hkv),
+ *     over j <= t with j > t - window or j < sinks.
+ * Storage: HCSA_BF16 or HCSA_F32.  Products, softmax statistics and sums are fp32 for both types (unlike
+ * the other fp32-storage calls, which compute in fp64): the result is rounded once when stored; the
+ * tensor-core paths also round each softmax weight to bf16 for the value product.
+ * H / Hkv <= 128 and dh <= 512; other shapes return HCSA_ERR_UNSUPPORTED. */
+
+/* Bytes of one of the two page arrays (n_pages, Hkv, page, dh, dtype, lowprec); 0 for a NULL p. */
+size_t hcsa_page_bytes(const hcsa_params *p);
+
+/* Causal prefill of one sequence of p->T tokens (or its row range p->row0 .. p->row1: such a call reads no
+ * key / value row outside [row0 - window + 1, row1) and [0, sinks)).
+ *   q [T, ld_q] (H*dh used, head-major), k [T, ld_k], v [T, ld_v] (Hkv*dh used each), out [T, ld_out] (H*dh
+ *   columns written).  A key or value that no query of a row may see never reaches that row, whatever it
+ *   holds (infinities and NaN included). */
+hcsa_status swa_attend(const hcsa_params *p, const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                       const void *v, int64_t ld_v, void *out, int64_t ld_out, void *stream);
+
+/* Write new tokens' keys and values into the pages: row r goes to token pos[r] of sequence seq[r] (seq NULL:
+ * sequence r, rows <= B).  k [rows, ld_k], v [rows, ld_v] (Hkv*dh used), pos, seq [rows] int32 (device).  A row
+ * with a negative pos or seq is skipped (an empty slot of the batch).  No two rows may name the same token.  A
+ * position past the sequence's pages, a sequence outside [0, B) or a page outside [0, n_pages) writes
+ * nothing and records HCSA_ERR_DEVICE.  p->lowprec: stored in 8 bits, one rounding (nearest, ties to even);
+ * exponents are held to [-126, 120], an infinite value stays infinite
+ * and a finite one finite. */
+hcsa_status swa_page_append(const hcsa_params *p, const hcsa_pages *pages, int64_t rows, const int32_t *pos,
+                            const int32_t *seq, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                            void *stream);
+
+/* Decode: attention of one new token per sequence over the pages, split over the keys and joined.
+ *   pos [B] int32 (device): position of the new token, whose key and value are in the pages already; -1:
+ *   an empty slot, whose output row is zeros.  q [B, ld_q], out [B, ld_out].
+ *   ws: hcsa_workspace_bytes(p, HCSA_OP_SWA_DECODE_ATTEND) bytes (contents need not be kept or cleared
+ *   between calls; calls that may overlap need one each).
+ * Rows of a page behind the sequence's last token are never used, whatever they hold.  A position past the
+ * sequence's pages or a page outside [0, n_pages) records HCSA_ERR_DEVICE; that sequence's output row is
+ * then unspecified, the others are right. */
+hcsa_status swa_decode_attend(const hcsa_params *p, const hcsa_pages *pages, const int32_t *pos, const void *q,
+                              int64_t ld_q, void *out, int64_t ld_out, void *ws, size_t ws_bytes, void *stream);
+
+/* Residual addition and root-mean-square norm between two layers of a chained stack (the pages define no
+ * normalisation; this is the usual one):
+ *     s = x + delta,  x_out = round(s),  y = s / sqrt(mean(s^2) + eps) * w
+ * with s and the mean in fp32 or wider, each result rounded once.
+ *   x [rows, ld_x]; delta [rows, ld_delta] or NULL (s = x); w [D]; x_out [rows, ld_xo] or NULL, may be x itself
+ *   y  [rows, ld_y] in p->dtype, or NULL
+ *   y8 or NULL (bf16 layers, D a multiple of 32): y in the FP8 layout of hcsa_params.lowprec: rows x D
+ *      bytes of E4M3 codes, then rows x D/32 int8 exponents, rounded once from y (not from its bf16 value);
+ *      each exponent is the one of the exact y even where a block's maximum lies next to a power-of-two
+ *      border, and is held to [-126, 120].
+ * One of y and y8 at least; D at most 16384.  Reads p->D and p->dtype only. */
+hcsa_status hcsa_add_rmsnorm(const hcsa_params *p, int64_t rows, const void *x, int64_t ld_x, const void *delta,
+                             int64_t ld_delta, const void *w, float eps, void *x_out, int64_t ld_xo, void *y,
+                             int64_t ld_y, void *y8, void *stream);
 
 /* Waits for `stream`, then returns and clears the device status word of the current device
  * (HCSA_OK, HCSA_ERR_TIMEOUT or HCSA_ERR_DEVICE), or HCSA_ERR_CUDA if the wait itself failed. */

@@ -15,10 +15,12 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libhcsa.so")
 
 HCSA_F32, HCSA_BF16 = 0, 1
-KIND_CSA, KIND_HCA = 0, 1
+KIND_CSA, KIND_HCA, KIND_SWA = 0, 1, 2
 OP_PROJECT, OP_CSA_INDEX_TOPK, OP_CSA_ATTEND, OP_HCA_ATTEND = 0, 1, 2, 3
 OP_CSA_DECODE_INDEX_TOPK, OP_CSA_DECODE_ATTEND, OP_HCA_DECODE_ATTEND = 4, 5, 6
 OP_CSA_DECODE_INDEX_TOPK_SHARD, OP_CSA_DECODE_ATTEND_SHARD, OP_HCA_DECODE_ATTEND_SHARD = 7, 8, 9
+OP_SWA_DECODE_ATTEND = 10
+NO_WINDOW = 2 ** 31 - 1   # window of a sliding-window layer that sees every earlier token
 
 STATUS = {0: "HCSA_OK", 1: "HCSA_ERR_NULL", 2: "HCSA_ERR_SHAPE", 3: "HCSA_ERR_DTYPE", 4: "HCSA_ERR_ALIGN",
           5: "HCSA_ERR_WORKSPACE", 6: "HCSA_ERR_CUDA", 7: "HCSA_ERR_TIMEOUT", 8: "HCSA_ERR_UNSUPPORTED",
@@ -32,7 +34,8 @@ EXPORTS = ["hcsa_version", "hcsa_status_string", "hcsa_workspace_bytes", "hcsa_p
            "hcsa_get_device_status", "hcsa_selftest_wait_timeout",
            "hcsa_launch_count", "hcsa_entry_bytes", "hcsa_key_bytes", "hcsa_quantize_rows",
            "csa_decode_index_topk_shard", "csa_topk_merge", "csa_decode_attend_shard", "hca_decode_attend_shard",
-           "hcsa_merge_partials", "hcsa_project_append", "hcsa_project_compress"]
+           "hcsa_merge_partials", "hcsa_project_append", "hcsa_project_compress",
+           "hcsa_page_bytes", "swa_attend", "swa_page_append", "swa_decode_attend", "hcsa_add_rmsnorm"]
 STORE_ENTRIES, STORE_KEYS = 0, 1
 
 
@@ -47,11 +50,18 @@ class Params(ctypes.Structure):
                                               "H", "dh")] + [("scale", ctypes.c_float), ("dtype", ctypes.c_int32),
                                                              ("n_cap", ctypes.c_int32), ("row0", ctypes.c_int32),
                                                              ("row1", ctypes.c_int32), ("lowprec", ctypes.c_int32),
-                                                             ("ent0", ctypes.c_int32), ("ent_shard", ctypes.c_int32)]
+                                                             ("ent0", ctypes.c_int32), ("ent_shard", ctypes.c_int32),
+                                                             ("Hkv", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                                                             ("page", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                                                             ("max_pages", ctypes.c_int32)]
 
 
 class Cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("entries", "idx_keys", "win_kv", "ring_g", "ring_ki")]
+
+
+class Pages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "page_table")]
 
 
 _lib = None
@@ -68,6 +78,7 @@ def load():
     V, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     P = ctypes.POINTER(Params)
     CP = ctypes.POINTER(Cache)
+    PG = ctypes.POINTER(Pages)
     sig = {
         "hcsa_version": (I32, []),
         "hcsa_status_string": (ctypes.c_char_p, [I32]),
@@ -98,6 +109,11 @@ def load():
         "hcsa_merge_partials": (I32, [P, V, I32, V, I64, V]),
         "hcsa_project_append": (I32, [P, I32, CP, V, V, V, V, V, V, SZ, V]),
         "hcsa_project_compress": (I32, [P, I32, V, V, V, V, V, V, V, SZ, V]),
+        "hcsa_page_bytes": (SZ, [P]),
+        "swa_attend": (I32, [P, V, I64, V, I64, V, I64, V, I64, V]),
+        "swa_page_append": (I32, [P, PG, I64, V, V, V, I64, V, I64, V]),
+        "swa_decode_attend": (I32, [P, PG, V, V, I64, V, I64, V, SZ, V]),
+        "hcsa_add_rmsnorm": (I32, [P, I64, V, I64, V, I64, V, ctypes.c_float, V, I64, V, I64, V, V]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -127,10 +143,12 @@ def _stream(stream):
 
 
 def make_params(*, T=0, D=0, m=4, width=8, C=0, di=0, Hi=0, topk=0, window=128, H=1, dh=0, scale=1.0,
-                dtype="bf16", B=1, n_cap=0, row0=0, row1=0, lowprec=0, ent0=0, ent_shard=0) -> Params:
+                dtype="bf16", B=1, n_cap=0, row0=0, row1=0, lowprec=0, ent0=0, ent_shard=0, Hkv=0, sinks=0, page=0,
+                n_pages=0, max_pages=0) -> Params:
     return Params(B=B, T=T, D=D, m=m, width=width, C=C, di=di, Hi=Hi, topk=topk, window=window, H=H, dh=dh,
                   scale=scale, dtype=HCSA_BF16 if dtype == "bf16" else HCSA_F32, n_cap=n_cap, row0=row0,
-                  row1=row1, lowprec=int(lowprec), ent0=ent0, ent_shard=int(ent_shard))
+                  row1=row1, lowprec=int(lowprec), ent0=ent0, ent_shard=int(ent_shard), Hkv=Hkv, sinks=sinks,
+                  page=page, n_pages=n_pages, max_pages=max_pages)
 
 
 def make_cache(entries, win_kv, ring_g, idx_keys=None, ring_ki=None) -> Cache:
@@ -296,3 +314,114 @@ def hcsa_merge_partials(p, parts, n_parts, out, stream=None):
 
 def hcsa_launch_count(reset: bool = False) -> int:
     return int(load().hcsa_launch_count(1 if reset else 0))
+
+
+# ---------------------------------------------------------------- sliding-window layers
+
+_TORCH = {HCSA_F32: torch.float32, HCSA_BF16: torch.bfloat16}
+
+
+def make_pages(k_pages, v_pages, page_table) -> Pages:
+    """The two page arrays ([n_pages, Hkv, page, dh], or FP8 byte arrays) and the [B, max_pages] int32 table.  The
+    handle keeps the tensors alive."""
+    if page_table.dtype != torch.int32 or not (page_table.is_contiguous() and k_pages.is_contiguous()
+                                               and v_pages.is_contiguous()):
+        raise HcsaError("make_pages", 2)
+    pages = Pages(k_pages=_ptr(k_pages), v_pages=_ptr(v_pages), page_table=_ptr(page_table))
+    pages.tensors = (k_pages, v_pages, page_table)
+    return pages
+
+
+def _rows2d(fn, t, dtype, rows, cols):
+    """A [rows, cols] tensor of the call's type whose columns are contiguous (what the C call cannot see); a
+    single row's stride does not matter.  Returns its leading dimension."""
+    if t.dtype != dtype:
+        raise HcsaError(fn, 3)
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        raise HcsaError(fn, 2)
+    return t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0))
+
+
+def _vec32(fn, t, n):
+    if t.dtype != torch.int32:
+        raise HcsaError(fn, 3)
+    if t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
+        raise HcsaError(fn, 2)
+
+
+def _check_pages(fn, p, pages):
+    k, v, table = pages.tensors
+    need = int(load().hcsa_page_bytes(ctypes.byref(p)))
+    dt = torch.uint8 if p.lowprec else _TORCH.get(p.dtype)
+    if k.dtype != dt or v.dtype != dt:
+        raise HcsaError(fn, 3)
+    if (k.numel() * k.element_size() < need or v.numel() * v.element_size() < need
+            or table.numel() < p.B * p.max_pages):
+        raise HcsaError(fn, 2)
+
+
+class _on:
+    """The device of a call's tensors as the current one (they may live on another)."""
+
+    def __init__(self, t):
+        self.guard = torch.cuda.device(t.device) if t.is_cuda and t.device.index != torch.cuda.current_device() else None
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def hcsa_page_bytes(p: Params) -> int:
+    return int(load().hcsa_page_bytes(ctypes.byref(p)))
+
+
+def swa_attend(p, q, k, v, out, stream=None):
+    """q, out: [T, H * dh]; k, v: [T, Hkv * dh] (column views of one projection are fine)."""
+    dt, n, nkv = _TORCH.get(p.dtype), p.H * p.dh, p.Hkv * p.dh
+    ld = [_rows2d("swa_attend", t, dt, p.T, c) for t, c in ((q, n), (k, nkv), (v, nkv), (out, n))]
+    with _on(q):
+        _check("swa_attend", load().swa_attend(ctypes.byref(p), _ptr(q), ld[0], _ptr(k), ld[1], _ptr(v), ld[2],
+                                               _ptr(out), ld[3], _stream(stream)))
+
+
+def swa_page_append(p, pages: Pages, pos, k, v, seq=None, stream=None):
+    """Write k, v [rows, Hkv * dh] to tokens pos[r] of sequences seq[r] (default: sequence r); pos[r] < 0: skipped."""
+    fn, dt, nkv, rows = "swa_page_append", _TORCH.get(p.dtype), p.Hkv * p.dh, k.shape[0]
+    ld = [_rows2d(fn, t, dt, rows, nkv) for t in (k, v)]
+    _vec32(fn, pos, rows)
+    if seq is not None:
+        _vec32(fn, seq, rows)
+    _check_pages(fn, p, pages)
+    with _on(k):
+        _check(fn, load().swa_page_append(ctypes.byref(p), ctypes.byref(pages), rows, _ptr(pos), _ptr(seq), _ptr(k),
+                                          ld[0], _ptr(v), ld[1], _stream(stream)))
+
+
+def swa_decode_attend(p, pages: Pages, pos, q, out, ws=None, stream=None):
+    """q, out: [B, H * dh]; pos[b]: position of the new token (already in the pages), -1 for an empty slot."""
+    fn, dt, n = "swa_decode_attend", _TORCH.get(p.dtype), p.H * p.dh
+    ld = [_rows2d(fn, t, dt, p.B, n) for t in (q, out)]
+    _vec32(fn, pos, p.B)
+    _check_pages(fn, p, pages)
+    with _on(q):
+        _check(fn, load().swa_decode_attend(ctypes.byref(p), ctypes.byref(pages), _ptr(pos), _ptr(q), ld[0], _ptr(out),
+                                            ld[1], _ptr(ws), _wsz(ws), _stream(stream)))
+
+
+def hcsa_add_rmsnorm(p, x, delta, w, eps, x_out, y, y8=None, stream=None):
+    """x_out = x + delta, y = rmsnorm(x + delta) * w ([rows, D]); delta, x_out, y or y8 (a byte buffer of
+    rows * (D + D / 32), FP8 layout) may be None."""
+    fn, dt, D, rows = "hcsa_add_rmsnorm", _TORCH.get(p.dtype), p.D, x.shape[0]
+    ld = [0 if t is None else _rows2d(fn, t, dt, rows, D) for t in (x, delta, x_out, y)]
+    if w.dtype != dt or (y8 is not None and y8.dtype != torch.uint8):
+        raise HcsaError(fn, 3)
+    if w.shape != (D,) or not w.is_contiguous() or (
+            y8 is not None and (y8.numel() < rows * (D + D // 32) or not y8.is_contiguous())):
+        raise HcsaError(fn, 2)
+    with _on(x):
+        _check(fn, load().hcsa_add_rmsnorm(ctypes.byref(p), rows, _ptr(x), ld[0], _ptr(delta), ld[1], _ptr(w), eps,
+                                           _ptr(x_out), ld[2], _ptr(y), ld[3], _ptr(y8), _stream(stream)))

@@ -4,6 +4,7 @@
 #include <stdio.h>
 
 #include "internal.cuh"
+#include "sliding.cuh"
 
 namespace hcsa {
 
@@ -104,6 +105,31 @@ hcsa_status row_range(const hcsa_params *p, int64_t *r0, int64_t *r1) {
     return HCSA_OK;
 }
 
+// A sliding-window layer: grouped heads, key and value of dh channels each.
+hcsa_status check_swa(const hcsa_params *p) {
+    HCSA_TRY(check_common(p));
+    if (p->Hkv < 1 || p->H % p->Hkv != 0 || p->sinks < 0) return HCSA_ERR_SHAPE;
+    if (p->H / p->Hkv > 128 || p->dh > 512 || p->T > (1 << 30)) return HCSA_ERR_UNSUPPORTED;
+    return HCSA_OK;
+}
+
+hcsa_status check_pages(const hcsa_params *p, const hcsa_pages *g) {
+    HCSA_TRY(check_swa(p));
+    if (!g || !g->k_pages || !g->v_pages || !g->page_table) return HCSA_ERR_NULL;
+    if (p->B < 1 || p->page < 16 || p->page % 16 != 0 || p->n_pages < 1 || p->max_pages < 1) return HCSA_ERR_SHAPE;
+    if (p->lowprec && p->dh % 32 != 0) return HCSA_ERR_UNSUPPORTED;
+    // rows of the page arrays and positions of a sequence are 32-bit; a position also has room for a chunk more
+    if ((int64_t)p->n_pages * p->Hkv > INT32_MAX / p->page || p->max_pages > (1 << 30) / p->page)
+        return HCSA_ERR_UNSUPPORTED;
+    if (!aligned(g->k_pages) || !aligned(g->v_pages) || ((uintptr_t)g->page_table & 3u)) return HCSA_ERR_ALIGN;
+    return HCSA_OK;
+}
+
+PageArgs page_args(const hcsa_params *p, const hcsa_pages *g) {
+    return PageArgs{p->dtype, p->lowprec != 0, p->B, p->Hkv, p->dh, p->page, p->n_pages, p->max_pages,
+                    g->k_pages, g->v_pages, g->page_table, device_status_ptr()};
+}
+
 // Entries whose pools end in rows [r0, r1): j in [r0 / m, ceil(r1 / m)) (r1 < T is a multiple of m).
 void entry_range(const hcsa_params *p, int64_t r0, int64_t r1, int64_t *j0, int64_t *j1) {
     *j0 = r0 / p->m;
@@ -149,6 +175,7 @@ const char *hcsa_status_string(hcsa_status s) {
 
 int64_t hcsa_proj_cols(const hcsa_params *p, int32_t kind) {
     if (!p) return -1;
+    if (kind == HCSA_KIND_SWA) return ((int64_t)p->H + 2 * (int64_t)p->Hkv) * p->dh;
     int64_t c = 2 * (int64_t)p->C + (int64_t)p->H * p->dh;
     if (kind == HCSA_KIND_CSA) c += (int64_t)p->di + (int64_t)p->Hi * p->di + p->Hi;
     return c;
@@ -189,6 +216,8 @@ size_t hcsa_workspace_bytes(const hcsa_params *p, int32_t op) {
         case HCSA_OP_CSA_DECODE_ATTEND_SHARD:
             return align256((size_t)p->B * p->topk * sizeof(int32_t)) + shard_part_ws(p, false);
         case HCSA_OP_HCA_DECODE_ATTEND_SHARD: return shard_part_ws(p, true);
+        case HCSA_OP_SWA_DECODE_ATTEND:
+            return check_swa(p) == HCSA_OK && p->B > 0 ? swa_decode_ws_bytes(p->B, p->H, p->Hkv, p->dh) : 0;
     }
     return 0;
 }
@@ -197,6 +226,7 @@ hcsa_status hcsa_project(const hcsa_params *p, int32_t kind, int64_t rows, const
                          void *y, void *ws, size_t ws_bytes, void *stream) {
     if (kind == HCSA_KIND_CSA) HCSA_TRY(check_csa(p));
     else if (kind == HCSA_KIND_HCA) HCSA_TRY(check_common(p));
+    else if (kind == HCSA_KIND_SWA) HCSA_TRY(check_swa(p));
     else return HCSA_ERR_SHAPE;
     if (!x || !W_cat || !y) return HCSA_ERR_NULL;
     if (rows < 0 || p->D < 1) return HCSA_ERR_SHAPE;
@@ -526,6 +556,75 @@ hcsa_status hcsa_merge_partials(const hcsa_params *p, const float *parts, int32_
     const int64_t nacc = (int64_t)p->B * p->H * p->dh, blk = nacc + 2 * (int64_t)p->B * p->H;
     return launch_merge_parts(parts, parts + nacc, blk, (int64_t)p->H * p->dh, blk / 2, p->H, n_parts, p->B, p->H,
                               p->dh, out, nullptr, nullptr, (cudaStream_t)stream);
+}
+
+// ---------------------------------------------------------------- sliding-window layers
+size_t hcsa_page_bytes(const hcsa_params *p) {
+    if (!p || p->n_pages < 0 || p->Hkv < 0 || p->page < 0 || p->dh < 0) return 0;
+    const size_t rows = (size_t)p->n_pages * p->Hkv * p->page;
+    return p->lowprec ? rows * (p->dh + p->dh / 32) : rows * p->dh * esize(p->dtype);
+}
+
+hcsa_status swa_attend(const hcsa_params *p, const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v,
+                       int64_t ld_v, void *out, int64_t ld_out, void *stream) {
+    HCSA_TRY(check_swa(p));
+    if (p->lowprec) return HCSA_ERR_UNSUPPORTED;
+    if (!q || !k || !v || !out) return HCSA_ERR_NULL;
+    if (p->T < 0) return HCSA_ERR_SHAPE;
+    if (!aligned(q) || !aligned(k) || !aligned(v) || !aligned(out)) return HCSA_ERR_ALIGN;
+    const int64_t n = (int64_t)p->H * p->dh, nkv = (int64_t)p->Hkv * p->dh;
+    if (!ld_ok(p->dtype, ld_q, n) || !ld_ok(p->dtype, ld_k, nkv) || !ld_ok(p->dtype, ld_v, nkv) ||
+        !ld_ok(p->dtype, ld_out, n))
+        return HCSA_ERR_ALIGN;
+    int64_t r0, r1;
+    HCSA_TRY(row_range(p, &r0, &r1));
+    if (r1 <= r0) return HCSA_OK;
+    SwaArgs a{p->dtype, p->T, p->H, p->Hkv, p->dh, p->window, p->sinks, p->scale, q, ld_q, k, ld_k, v, ld_v, out,
+              ld_out, (int)r0, (int)r1, device_status_ptr()};
+    return launch_swa(a, (cudaStream_t)stream);
+}
+
+hcsa_status swa_page_append(const hcsa_params *p, const hcsa_pages *pages, int64_t rows, const int32_t *pos,
+                            const int32_t *seq, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                            void *stream) {
+    HCSA_TRY(check_pages(p, pages));
+    if (!pos || !k || !v) return HCSA_ERR_NULL;
+    if (rows < 0 || (!seq && rows > p->B)) return HCSA_ERR_SHAPE;
+    if (!aligned(k) || !aligned(v) || ((uintptr_t)pos & 3u) || ((uintptr_t)seq & 3u)) return HCSA_ERR_ALIGN;
+    const int64_t nkv = (int64_t)p->Hkv * p->dh;
+    if (!ld_ok(p->dtype, ld_k, nkv) || !ld_ok(p->dtype, ld_v, nkv)) return HCSA_ERR_ALIGN;
+    return launch_page_append(page_args(p, pages), rows, pos, seq, k, ld_k, v, ld_v, (cudaStream_t)stream);
+}
+
+hcsa_status swa_decode_attend(const hcsa_params *p, const hcsa_pages *pages, const int32_t *pos, const void *q,
+                              int64_t ld_q, void *out, int64_t ld_out, void *ws, size_t ws_bytes, void *stream) {
+    HCSA_TRY(check_pages(p, pages));
+    if (!pos || !q || !out) return HCSA_ERR_NULL;
+    if (!aligned(q) || !aligned(out) || !aligned(ws) || ((uintptr_t)pos & 3u)) return HCSA_ERR_ALIGN;
+    const int64_t n = (int64_t)p->H * p->dh;
+    if (!ld_ok(p->dtype, ld_q, n) || !ld_ok(p->dtype, ld_out, n)) return HCSA_ERR_ALIGN;
+    if (!ws || ws_bytes < hcsa_workspace_bytes(p, HCSA_OP_SWA_DECODE_ATTEND)) return HCSA_ERR_WORKSPACE;
+    DecodeArgs a{page_args(p, pages), p->H, p->window, p->sinks, p->scale, pos, q, ld_q, out, ld_out, ws};
+    return launch_swa_decode(a, (cudaStream_t)stream);
+}
+
+hcsa_status hcsa_add_rmsnorm(const hcsa_params *p, int64_t rows, const void *x, int64_t ld_x, const void *delta,
+                             int64_t ld_delta, const void *w, float eps, void *x_out, int64_t ld_xo, void *y,
+                             int64_t ld_y, void *y8, void *stream) {
+    if (!p) return HCSA_ERR_NULL;
+    if (p->dtype != HCSA_F32 && p->dtype != HCSA_BF16) return HCSA_ERR_DTYPE;
+    if (!x || !w || (!y && !y8)) return HCSA_ERR_NULL;
+    if (rows < 0 || p->D < 1 || !(eps >= 0.f)) return HCSA_ERR_SHAPE;
+    if (y8 && (p->dtype != HCSA_BF16 || p->D % 32 != 0)) return HCSA_ERR_UNSUPPORTED;
+    if (p->D > 16384 || rows > INT32_MAX) return HCSA_ERR_UNSUPPORTED;
+    if (!aligned(x) || !aligned(delta) || !aligned(w) || !aligned(x_out) || !aligned(y) || !aligned(y8) ||
+        p->D % vec(p->dtype) != 0)
+        return HCSA_ERR_ALIGN;
+    if (!ld_ok(p->dtype, ld_x, p->D) || (delta && !ld_ok(p->dtype, ld_delta, p->D)) ||
+        (x_out && !ld_ok(p->dtype, ld_xo, p->D)) || (y && !ld_ok(p->dtype, ld_y, p->D)))
+        return HCSA_ERR_ALIGN;
+    NormArgs a{p->dtype, rows, p->D, x, ld_x, delta, ld_delta, w, eps, x_out, ld_xo, y, ld_y, y8};
+    return launch_add_rmsnorm(a, (cudaStream_t)stream);
 }
 
 hcsa_status hcsa_get_device_status(void *stream) {

@@ -1,0 +1,199 @@
+// Sliding-window layers: the key sets of prefill blocks and decode steps, the argument structs of the
+// launchers, and the exact recomputation of single rows.
+#pragma once
+
+#include "internal.cuh"
+#include "lowprec.cuh"
+
+namespace hcsa {
+
+// ---------------------------------------------------------------- norm (norm.cu)
+struct NormArgs {
+    int dtype;
+    int64_t rows;
+    int D;
+    const void *x; int64_t ld_x;
+    const void *delta; int64_t ld_delta;   // nullptr: no addition
+    const void *w;
+    float eps;
+    void *x_out; int64_t ld_xo;            // nullptr: not stored
+    void *y; int64_t ld_y;                 // nullptr: not stored
+    void *y8;                              // FP8 codes + exponents, or nullptr
+};
+hcsa_status launch_add_rmsnorm(const NormArgs &a, cudaStream_t st);
+
+// ---------------------------------------------------------------- prefill
+// fp32 storage of an fp32 result
+__device__ __forceinline__ void store_val(float *p, float v) { *p = v; }
+
+struct SwaArgs {
+    int dtype;
+    int T, H, Hkv, dh, window, sinks;
+    float scale;
+    const void *q; int64_t ld_q;
+    const void *k; int64_t ld_k;
+    const void *v; int64_t ld_v;
+    void *out; int64_t ld_out;
+    int row0, row1;                        // query rows computed
+    int *status;
+};
+hcsa_status launch_swa(const SwaArgs &a, cudaStream_t st);        // chooses the kernel
+hcsa_status launch_swa_simt(const SwaArgs &a, cudaStream_t st);
+
+// Keys of a block of consecutive queries [t_first, t_last]: `pad` columns for the first tokens that lie
+// outside the window of the block's first query (n_sink of them real), then one column per token from w0
+// to t_last.  Column c holds token c (c < pad) or w0 + c - pad.
+struct BlockKeys {
+    int n_sink, pad, w0, n;
+    __device__ __forceinline__ int token(int c) const { return c < pad ? c : w0 + c - pad; }
+};
+__device__ __forceinline__ BlockKeys block_keys(int t_first, int t_last, int window, int sinks, int granule) {
+    BlockKeys b;
+    b.w0 = t_first - window + 1 > 0 ? t_first - window + 1 : 0;
+    b.n_sink = sinks < b.w0 ? sinks : b.w0;
+    b.pad = (b.n_sink + granule - 1) / granule * granule;
+    b.n = b.pad + t_last - b.w0 + 1;
+    return b;
+}
+// Is column c of the block seen by query t?
+__device__ __forceinline__ bool column_seen(const BlockKeys &b, int c, int t, int window, int sinks) {
+    if (c < b.pad) return c < b.n_sink;
+    const int j = b.w0 + c - b.pad;
+    return j <= t && (j > t - window || j < sinks);
+}
+
+// The blocked kernels give every masked key the weight 0, and 0 times a masked value that is infinite or NaN
+// is NaN.  So a row that comes out non-finite is looked at again by one warp: if a value that its block
+// loaded and the row does not see is non-finite, the row is computed once more over exactly its keys; else
+// it is non-finite by its own keys and values and stays.
+
+// Is a value of key head g in tokens [lo, hi) infinite or NaN?
+template <typename S>
+__device__ bool values_bad(const SwaArgs &a, int g, int64_t lo, int64_t hi, int lane) {
+    bool bad = false;
+    for (int64_t j = lo; j < hi; ++j) {
+        const S *v = (const S *)a.v + j * a.ld_v + (int64_t)g * a.dh;
+        for (int d = lane; d < a.dh; d += 32) bad = bad || !(fabsf((float)v[d]) < INFINITY);
+    }
+    return __any_sync(0xffffffffu, bad);
+}
+// Row (t, h) over exactly the keys it sees, by one warp.  Ends early once every channel is NaN, which no
+// further key can change (so a sequence full of NaN does not cost a key-by-key pass per row).
+template <typename S>
+__device__ void attend_row(const SwaArgs &a, int t, int h, int lane) {
+    const int g = h / (a.H / a.Hkv);
+    const S *q = (const S *)a.q + (int64_t)t * a.ld_q + (int64_t)h * a.dh;
+    const S *k = (const S *)a.k + (int64_t)g * a.dh;
+    const S *v = (const S *)a.v + (int64_t)g * a.dh;
+    float acc[16], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    const int w0 = t - a.window + 1 > 0 ? t - a.window + 1 : 0;
+    const int ns = a.sinks < w0 ? a.sinks : w0;
+    for (int64_t c = 0; c < (int64_t)ns + (t - w0 + 1); ++c) {
+        const int64_t j = c < ns ? c : w0 + (c - ns);
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int d = lane + 32 * i;
+            if (d < a.dh) s += (float)q[d] * (float)k[j * a.ld_k + d];
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        s *= a.scale * 1.4426950408889634f;
+        const float mn = fmaxf(m, s);
+        const float f = mn == -INFINITY ? 1.f : exp2f(m - mn);
+        const float p = s == -INFINITY && mn == -INFINITY ? 0.f : exp2f(s - mn);
+        m = mn;
+        l = l * f + p;
+        bool lost = true;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int d = lane + 32 * i;
+            if (d < a.dh) {
+                acc[i] = acc[i] * f + p * (float)v[j * a.ld_v + d];
+                lost = lost && acc[i] != acc[i];
+            }
+        }
+        if (__all_sync(0xffffffffu, lost || l != l)) break;
+    }
+    S *o = (S *)a.out + (int64_t)t * a.ld_out + (int64_t)h * a.dh;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int d = lane + 32 * i;
+        if (d < a.dh) store_val(o + d, acc[i] / l);
+    }
+}
+
+// ---------------------------------------------------------------- paged cache
+constexpr int kChunk16 = 16;               // tokens per chunk; a chunk never crosses a page
+
+struct PageArgs {
+    int dtype;
+    bool lowprec;
+    int B, Hkv, dh, page, n_pages, max_pages;
+    void *k_pages, *v_pages;
+    const int32_t *table;
+    int *status;
+};
+hcsa_status launch_page_append(const PageArgs &a, int64_t rows, const int32_t *pos, const int32_t *seq, const void *k,
+                               int64_t ld_k, const void *v, int64_t ld_v, cudaStream_t st);
+
+struct DecodeArgs {
+    PageArgs c;
+    int H, window, sinks;
+    float scale;
+    const int32_t *pos;
+    const void *q; int64_t ld_q;
+    void *out; int64_t ld_out;
+    void *ws;
+};
+size_t swa_decode_ws_bytes(int B, int H, int Hkv, int dh);
+hcsa_status launch_swa_decode(const DecodeArgs &a, cudaStream_t st);
+
+// Chunks of 16 tokens that the new token of a sequence reads: those of the first tokens, then those from
+// the window's first chunk on (from token 0 when the two meet).
+struct DecodeKeys {
+    int pos, w0, n_far, far_end, n;        // far_end: token of chunk n_far (the window's first chunk)
+    __device__ __forceinline__ int token(int c) const { return c < n_far ? 16 * c : far_end + 16 * (c - n_far); }
+};
+__device__ __forceinline__ DecodeKeys decode_keys(int pos, int window, int sinks, int64_t capacity, int *status) {
+    DecodeKeys k{pos, 0, 0, 0, 0};
+    if (pos < 0) return k;
+    if (pos >= capacity) {
+        report(status, kStatusBounds);
+        return k;
+    }
+    k.w0 = pos - window + 1 > 0 ? pos - window + 1 : 0;
+    k.far_end = k.w0 & ~15;
+    k.n_far = ((sinks < k.w0 ? sinks : k.w0) + 15) >> 4;
+    if (16 * k.n_far >= k.far_end) k.n_far = k.far_end = 0;
+    k.n = k.n_far + ((pos - k.far_end) >> 4) + 1;
+    return k;
+}
+__device__ __forceinline__ bool token_seen(const DecodeKeys &k, int j, int sinks) {
+    return j <= k.pos && (j >= k.w0 || j < sinks);
+}
+
+// Exponent of a 32-channel block in the pages and the norm's output: the smallest e with
+// amax / 2^e <= 448, held to [-126, 120] so that 2^e and 2^-e are ordinary floats.
+__device__ __forceinline__ int page_exponent(float amax) {
+    if (!(amax < INFINITY)) return 120;
+    const int e = lp::block_exponent(amax, 1.75f, 8);
+    return e < -126 ? -126 : e;
+}
+// 8 channels -> 8 codes of x / 2^e (e in [-126, 120]); one rounding.  At e = 120 a finite value above 248 2^120
+// would round up to 2^128, which fp32 and bf16 hold as infinity: it takes the code 240 instead (within half a step).
+__device__ __forceinline__ uint2 codes_of(const float *v, int e) {
+    const float inv = lp::pow2f(-e);
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float t = v[i] * inv;
+        if (e == 120 && fabsf(t) < INFINITY) t = fminf(fmaxf(t, -240.f), 240.f);
+        w[i >> 2] |= ((uint32_t)__nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3) & 0xFFu) << (8 * (i & 3));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+}  // namespace hcsa

@@ -16,13 +16,17 @@ def torch_dtype(dtype: str):
     return torch.bfloat16 if dtype == "bf16" else torch.float32
 
 
-def params_for(spec, *, T=None, B=1, n_cap=0, row0=0, row1=0, lowprec=False, ent0=0, ent_shard=False) -> L.Params:
-    """Params from any object with the layer fields (kind, D, m, width, C, di, Hi, topk, window, H, dh, scale, dtype).
+def params_for(spec, *, T=None, B=1, n_cap=0, row0=0, row1=0, lowprec=False, ent0=0, ent_shard=False,
+               page=0, n_pages=0, max_pages=0) -> L.Params:
+    """Params from any object with the layer fields (kind, D, m, width, C, di, Hi, topk, window, H, dh, scale, dtype;
+    Hkv and sinks for a sliding-window layer, whose decode step also takes page, n_pages and max_pages).
     row0 / row1: the prefill row range (both 0: the whole sequence).  lowprec: FP8 entries, FP4 indexer keys."""
     return L.make_params(T=spec.T if T is None else T, D=spec.D, m=spec.m, width=spec.width, C=spec.C,
                          di=getattr(spec, "di", 0), Hi=getattr(spec, "Hi", 0), topk=getattr(spec, "topk", 0),
                          window=spec.window, H=spec.H, dh=spec.dh, scale=spec.scale, dtype=spec.dtype, B=B,
-                         n_cap=n_cap, row0=row0, row1=row1, lowprec=lowprec, ent0=ent0, ent_shard=ent_shard)
+                         n_cap=n_cap, row0=row0, row1=row1, lowprec=lowprec, ent0=ent0, ent_shard=ent_shard,
+                         Hkv=getattr(spec, "Hkv", 0), sinks=getattr(spec, "sinks", 0), page=page, n_pages=n_pages,
+                         max_pages=max_pages)
 
 
 def row_ranges(T, chunks):
