@@ -217,7 +217,7 @@ size_t hcsa_workspace_bytes(const hcsa_params *p, int32_t op) {
             return align256((size_t)p->B * p->topk * sizeof(int32_t)) + shard_part_ws(p, false);
         case HCSA_OP_HCA_DECODE_ATTEND_SHARD: return shard_part_ws(p, true);
         case HCSA_OP_SWA_DECODE_ATTEND:
-            return check_swa(p) == HCSA_OK && p->B > 0 ? swa_decode_ws_bytes(p->B, p->H, p->Hkv, p->dh) : 0;
+            return check_swa(p) == HCSA_OK && p->B > 0 ? swa_decode_ws_bytes(p->dtype, p->B, p->dh) : 0;
     }
     return 0;
 }

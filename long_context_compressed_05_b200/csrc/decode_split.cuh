@@ -108,5 +108,8 @@ bool decode_direct(const DecodeArgs &a);
 
 hcsa_status launch_decode_simt(const DecodeArgs &a, cudaStream_t st);
 int decode_simt_heads(int dh);
+bool decode_tc_supported(int dtype, int dh);
+int decode_tc_heads();
+hcsa_status launch_decode_tc(const DecodeArgs &a, cudaStream_t st);
 
 }  // namespace hcsa

@@ -148,7 +148,7 @@ struct DecodeArgs {
     void *out; int64_t ld_out;
     void *ws;
 };
-size_t swa_decode_ws_bytes(int B, int H, int Hkv, int dh);
+size_t swa_decode_ws_bytes(int dtype, int B, int dh);
 hcsa_status launch_swa_decode(const DecodeArgs &a, cudaStream_t st);
 
 // Chunks of 16 tokens that the new token of a sequence reads: those of the first tokens, then those from

@@ -360,10 +360,13 @@ hcsa_status launch_decode_simt(const DecodeArgs &a, cudaStream_t st) {
     return a.c.lowprec ? launch_dh<__nv_bfloat16, true>(a, st) : launch_dh<__nv_bfloat16, false>(a, st);
 }
 
-size_t swa_decode_ws_bytes(int B, int H, int Hkv, int dh) {
-    return decode_split_bytes(B, decode_grid(), decode_simt_heads(dh), dh);
+size_t swa_decode_ws_bytes(int dtype, int B, int dh) {
+    const int heads = decode_tc_supported(dtype, dh) ? decode_tc_heads() : decode_simt_heads(dh);
+    return decode_split_bytes(B, decode_grid(), heads, dh);
 }
 
-hcsa_status launch_swa_decode(const DecodeArgs &a, cudaStream_t st) { return launch_decode_simt(a, st); }
+hcsa_status launch_swa_decode(const DecodeArgs &a, cudaStream_t st) {
+    return decode_tc_supported(a.c.dtype, a.c.dh) ? launch_decode_tc(a, st) : launch_decode_simt(a, st);
+}
 
 }  // namespace hcsa

@@ -289,5 +289,8 @@ bool make_tmap_bf16_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t
 // host: encode a 2-D bf16 tensor map (dim 0 contiguous, row stride s1 bytes)
 bool make_tmap_bf16_2d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t s1, uint32_t b0,
                        uint32_t b1, bool swizzle128);
+// host: encode a 2-D map of bytes; the box's rows (b0 = 64 or 128 bytes) swizzled over their own width
+bool make_tmap_u8_2d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t s1, uint32_t b0,
+                     uint32_t b1);
 
 }  // namespace hcsa
