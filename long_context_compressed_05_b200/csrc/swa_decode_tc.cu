@@ -90,6 +90,10 @@ __device__ __forceinline__ void codes_any(uint32_t w, float lo, float hi, uint32
 }
 // any code of the word that is NaN (0x7F or 0xFF) leaves a bit in the sign positions
 __device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }
+// any of four exponents above 7 (the factor 2^(e + 120) would pass bf16's range) leaves a bit in the sign positions
+__device__ __forceinline__ uint32_t big_bits(uint32_t e) { return ((e & 0x78787878u) + 0x78787878u) & ~e; }
+// e + 247 of four exponents up to 7: the exponent field of 2^(e + 120)
+__device__ __forceinline__ uint32_t fields(uint32_t e) { return (e ^ 0x80808080u) + 0x77777777u; }
 
 // byte offset of granule g (16 bytes) of row r in a K or V tile, as the TMA box leaves it
 template <int DH, bool FP8>
@@ -238,7 +242,6 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                                (j0 >= dk.w0 || j0 + 15 < a.sinks);
             // the exponents of the four keys and two key columns this thread touches
             uint32_t ke[2] = {0, 0}, ve[4] = {0, 0, 0, 0};
-            bool fast = true;
             if constexpr (FP8) {
                 const uint8_t *ex = ring + (warp * NST + st) * Sh::kStage + 2 * Sh::kTile;
 #pragma unroll
@@ -273,18 +276,18 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                 tc::fence_async_smem();   // ordered before the next TMA write of this stage
                 __syncwarp();
             }
-            float sc[2][4];
+            float sc[2][4], sd[2][4];   // even and odd steps: two shorter chains of products
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[t][e] = 0.f;
+                for (int e = 0; e < 4; ++e) sc[t][e] = sd[t][e] = 0.f;
             if constexpr (!FP8) {
 #pragma unroll
                 for (int k = 0; k < NK; ++k) {
                     uint32_t b[4];
                     ldsm4(kt + tile_offset<DH, FP8>((lane & 7) + ((lane >> 4) & 1) * 8, 2 * k + ((lane >> 3) & 1)), b);
-                    mma16816(sc[0], q[k], b[0], b[1]);
-                    mma16816(sc[1], q[k], b[2], b[3]);
+                    mma16816(k & 1 ? sd[0] : sc[0], q[k], b[0], b[1]);
+                    mma16816(k & 1 ? sd[1] : sc[1], q[k], b[2], b[3]);
                 }
             } else {
                 uint32_t w[NK / 2][4], nan = 0;
@@ -294,26 +297,28 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) nan |= nan_bits(w[k][e]);
                 }
-                bool big = false;
+                if (!__any_sync(0xffffffffu, (nan | big_bits(ke[0]) | big_bits(ke[1])) & 0x80808080u)) {
+                    const uint32_t z[2] = {fields(ke[0]), fields(ke[1])};
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+                    for (int k = 0; k < NK / 2; ++k) {   // steps 2 k and 2 k + 1: block k
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) big = big || (int8_t)(ke[t] >> (8 * b)) > 7;
-                fast = !__any_sync(0xffffffffu, big || (nan & 0x80808080u));
-#pragma unroll
-                for (int k = 0; k < NK / 2; ++k) {   // steps 2 k and 2 k + 1: block k
-                    uint32_t b0, b1;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int t = e & 1;
-                        const int x = (int8_t)(ke[t] >> (8 * k));
-                        if (fast) {
-                            const uint32_t f = (uint32_t)(x + 247) << 7;
-                            codes_fast(w[k][e], f | (f << 16), b0, b1);
-                        } else {
-                            codes_any(w[k][e], lp::pow2f(x), lp::pow2f(x), b0, b1);
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t b0, b1;
+                            // byte k of z in both halves, in the place of a bf16 exponent
+                            codes_fast(w[k][e], __byte_perm(z[e & 1], 0, 0x4040 + 0x0101 * k) << 7, b0, b1);
+                            mma16816(e >> 1 ? sd[e & 1] : sc[e & 1], q[2 * k + (e >> 1)], b0, b1);
                         }
-                        mma16816(sc[t], q[2 * k + (e >> 1)], b0, b1);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < NK / 2; ++k) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t b0, b1;
+                            const float f = lp::pow2f((int8_t)(ke[e & 1] >> (8 * k)));
+                            codes_any(w[k][e], f, f, b0, b1);
+                            mma16816(e >> 1 ? sd[e & 1] : sc[e & 1], q[2 * k + (e >> 1)], b0, b1);
+                        }
                     }
                 }
             }
@@ -321,7 +326,7 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    sc[t][e] *= scale;
+                    sc[t][e] = (sc[t][e] + sd[t][e]) * scale;
                     if (!whole && !token_seen(dk, j0 + 8 * t + 2 * cq + (e & 1), a.sinks)) sc[t][e] = -INFINITY;
                 }
             float n0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
@@ -376,28 +381,38 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) nan |= nan_bits(w[j][e]);
                 }
-                bool big = false;
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+                for (int t = 0; t < 4; ++t) nan |= big_bits(ve[t]);
+                // granules 2 j and 2 j + 1 of the row: block j; t: keys 0..7, 8..15
+                if (!__any_sync(0xffffffffu, nan & 0x80808080u)) {
+                    const uint32_t z[4] = {fields(ve[0]), fields(ve[1]), fields(ve[2]), fields(ve[3])};
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) big = big || (int8_t)(ve[t] >> (8 * b)) > 7;
-                fast = !__any_sync(0xffffffffu, big || (nan & 0x80808080u));
+                    for (int j = 0; j < NK / 2; ++j) {
+                        uint32_t f[2];
 #pragma unroll
-                for (int j = 0; j < NK / 2; ++j) {   // granules 2 j and 2 j + 1: block j
-                    uint32_t e0[2], o0[2];
+                        for (int t = 0; t < 2; ++t) f[t] = (__byte_perm(z[2 * t], z[2 * t + 1], 0x0400 + 0x0101 * j) & 0x00FF00FFu) << 7;
 #pragma unroll
-                    for (int gi = 0; gi < 2; ++gi) {
+                        for (int gi = 0; gi < 2; ++gi) {
+                            uint32_t e0[2], o0[2];
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {   // keys 0..7, 8..15
-                            const int xa = (int8_t)(ve[2 * t] >> (8 * j)), xb = (int8_t)(ve[2 * t + 1] >> (8 * j));
-                            if (fast)
-                                codes_fast(w[j][2 * gi + t],
-                                           ((uint32_t)(xa + 247) << 7) | ((uint32_t)(xb + 247) << 23), e0[t], o0[t]);
-                            else
-                                codes_any(w[j][2 * gi + t], lp::pow2f(xa), lp::pow2f(xb), e0[t], o0[t]);
+                            for (int t = 0; t < 2; ++t) codes_fast(w[j][2 * gi + t], f[t], e0[t], o0[t]);
+                            mma16816(o[2 * (2 * j + gi)], p, e0[0], e0[1]);
+                            mma16816(o[2 * (2 * j + gi) + 1], p, o0[0], o0[1]);
                         }
-                        mma16816(o[2 * (2 * j + gi)], p, e0[0], e0[1]);
-                        mma16816(o[2 * (2 * j + gi) + 1], p, o0[0], o0[1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < NK / 2; ++j) {
+#pragma unroll
+                        for (int gi = 0; gi < 2; ++gi) {
+                            uint32_t e0[2], o0[2];
+#pragma unroll
+                            for (int t = 0; t < 2; ++t)
+                                codes_any(w[j][2 * gi + t], lp::pow2f((int8_t)(ve[2 * t] >> (8 * j))),
+                                          lp::pow2f((int8_t)(ve[2 * t + 1] >> (8 * j))), e0[t], o0[t]);
+                            mma16816(o[2 * (2 * j + gi)], p, e0[0], e0[1]);
+                            mma16816(o[2 * (2 * j + gi) + 1], p, o0[0], o0[1]);
+                        }
                     }
                 }
             }
