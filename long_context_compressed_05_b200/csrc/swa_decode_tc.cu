@@ -15,12 +15,18 @@
 // Keys that are not seen get weight 0, and their V rows are zeroed in shared memory before the product (0 x NaN is
 // NaN); only chunks at the ends of the visible ranges have any.
 //
-// FP8 codes become bf16 operands exactly: the seven exponent and mantissa bits placed at the bottom of bf16's
-// are the value times 2^-120, and one packed multiply by 2^(e + 120) restores it (blocks with e > 7 or NaN codes
-// take the conversion instructions).  Codes 2i and 2i + 2 of a word share a register, so the K channels and the
-// output channels run in a permuted order that the Q fragments and the stores follow.
+// FP8 pages run the products in fp16, whose conversion from E4M3 is one instruction for two codes: a code times
+// 2^(e - E), E a reference exponent of the warp, is an fp16 number when e lies in [E - 8, E + 7].  The K reference is
+// picked again for a chunk that leaves the range; the V reference (O is held times 2^-E) is raised with O rescaled;
+// a chunk whose exponents spread further takes the slow path: bf16 operands by full conversions.  Queries are scaled
+// per head to fp16 by a power of two where that is exact (a ratio of 2^32 between the largest and the smallest
+// channel), else the segment takes the slow path.  Weights are held times 2^15, so their rounding to fp16 is
+// relative (2^-11) down to 2^-29 of the largest.  Codes 2i and 2i + 1 of a word share a register (K), or two keys'
+// codes of one channel (V), so channels run in a permuted order that the Q fragments and the stores follow.
 #include "decode_split.cuh"
 #include "tc_common.cuh"
+
+#include <cuda_fp16.h>
 
 namespace hcsa {
 
@@ -64,36 +70,46 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+
+__device__ __forceinline__ void mma16816h(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2h(float lo, float hi) {
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-
-// Four codes -> bf16 of codes (0, 2) and (1, 3), times the factors `f` (2^(e + 120), one per half)
-__device__ __forceinline__ void codes_fast(uint32_t w, uint32_t f, uint32_t &even, uint32_t &odd) {
-    even = mul2(((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u), f);
-    odd = mul2(((w >> 4) & 0x07F007F0u) | (w & 0x80008000u), f);
+// four codes -> two registers of two fp16 (codes 0, 1 and 2, 3), each times its factors
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t f01, uint32_t f23, uint32_t &r01, uint32_t &r23) {
+    uint32_t x, y;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h;}"
+        : "=r"(x), "=r"(y) : "r"(w));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r01) : "r"(x), "r"(f01));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r23) : "r"(y), "r"(f23));
 }
-// the same by conversion instructions, for any exponent and NaN codes: lo, hi the scales of the two halves
-__device__ __forceinline__ void codes_any(uint32_t w, float lo, float hi, uint32_t &even, uint32_t &odd) {
+// the same in bf16 for any exponent: scale factors s0 .. s3 of the codes
+__device__ __forceinline__ void codes_bf16(uint32_t w, float s0, float s1, float s2, float s3, uint32_t &r01,
+                                           uint32_t &r23) {
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         __nv_fp8_e4m3 c;
         c.__x = (uint8_t)(w >> (8 * i));
-        v[i] = (float)c * (i < 2 ? lo : hi);
+        v[i] = (float)c;
     }
-    // V: bytes 0, 1 are of the low halves' key, 2, 3 of the high halves'; K: one key, lo == hi
-    even = pack2(v[0], v[2]);
-    odd = pack2(v[1], v[3]);
+    r01 = pack2(v[0] * s0, v[1] * s1);
+    r23 = pack2(v[2] * s2, v[3] * s3);
 }
-// any code of the word that is NaN (0x7F or 0xFF) leaves a bit in the sign positions
-__device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }
-// any of four exponents above 7 (the factor 2^(e + 120) would pass bf16's range) leaves a bit in the sign positions
-__device__ __forceinline__ uint32_t big_bits(uint32_t e) { return ((e & 0x78787878u) + 0x78787878u) & ~e; }
-// e + 247 of four exponents up to 7: the exponent field of 2^(e + 120)
-__device__ __forceinline__ uint32_t fields(uint32_t e) { return (e ^ 0x80808080u) + 0x77777777u; }
+__device__ __forceinline__ int max4s(uint32_t e) {   // largest of four signed bytes
+    int m = (int8_t)e;
+#pragma unroll
+    for (int b = 1; b < 4; ++b) m = max(m, (int)(int8_t)(e >> (8 * b)));
+    return m;
+}
+__device__ __forceinline__ float pow2_or_0(int e) { return e < -126 ? 0.f : lp::pow2f(e); }
 
 // byte offset of granule g (16 bytes) of row r in a K or V tile, as the TMA box leaves it
 template <int DH, bool FP8>
@@ -163,24 +179,20 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
         const int heads = G - h0 < kHB ? G - h0 : kHB;
         const int mine = sg.c1 - sg.c0 > warp ? (sg.c1 - sg.c0 - warp + kW - 1) / kW : 0;   // chunks of this warp
 
-        int ids = 0;                 // lane i: page of this warp's chunk (asked & ~31) + i
+        int lines = 0;               // lane i: first row of this warp's chunk (asked & ~31) + i in the page arrays
         int asked = 0;               // of this segment
         auto ask = [&]() {           // whole warp
-            if ((asked & 31) == 0) {
-                ids = 0;
-                if (asked + lane < mine) {
-                    const int j0 = dk.token(sg.c0 + warp + (asked + lane) * kW);
-                    ids = a.c.table[(int64_t)sg.b * a.c.max_pages + j0 / a.c.page];
-                    if (ids < 0 || ids >= a.c.n_pages) {
-                        report(a.c.status, kStatusBounds);
-                        ids = 0;
-                    }
+            if ((asked & 31) == 0 && asked + lane < mine) {
+                const int j0 = dk.token(sg.c0 + warp + (asked + lane) * kW), nth = j0 / a.c.page;
+                int id = a.c.table[(int64_t)sg.b * a.c.max_pages + nth];
+                if (id < 0 || id >= a.c.n_pages) {
+                    report(a.c.status, kStatusBounds);
+                    id = 0;
                 }
+                lines = (id * a.c.Hkv + g) * a.c.page + (j0 - nth * a.c.page);   // below 2^31 (checked on the host)
             }
-            const int id = __shfl_sync(0xffffffffu, ids, asked & 31);
+            const int line = __shfl_sync(0xffffffffu, lines, asked & 31);
             if (lane == 0) {
-                const int j0 = dk.token(sg.c0 + warp + asked * kW);
-                const int line = (id * a.c.Hkv + g) * a.c.page + j0 % a.c.page;   // below 2^31 (checked on the host)
                 const int st = it % NST;
                 const uint32_t dst = stages + st * Sh::kStage;
                 uint64_t *bar = &bars[warp][st];
@@ -191,8 +203,8 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                     tc::tma_load_2d(dst + Sh::kTile + c * 2048, &tm_v, c * 64, line, bar);
                 }
                 if constexpr (FP8) {
-                    const int64_t lines = (int64_t)a.c.n_pages * a.c.Hkv * a.c.page;
-                    const int64_t at = lines * DH + (int64_t)line * NB;
+                    const int64_t all = (int64_t)a.c.n_pages * a.c.Hkv * a.c.page;
+                    const int64_t at = all * DH + (int64_t)line * NB;
                     tc::bulk_load(dst + 2 * Sh::kTile, (const uint8_t *)a.c.k_pages + at, Sh::kExps, bar);
                     tc::bulk_load(dst + 2 * Sh::kTile + Sh::kExps, (const uint8_t *)a.c.v_pages + at, Sh::kExps, bar);
                 }
@@ -202,30 +214,61 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
         };
         for (int i = 0; i < NST && i < mine; ++i) ask();
 
-        // Q fragments: 16 heads x 16 channels a step; rows past the group are zero
-        uint32_t q[NK][4];
-        {
-            const __nv_bfloat16 *qr = (const __nv_bfloat16 *)a.q + (int64_t)sg.b * a.ld_q + (int64_t)(g * G + h0) * DH;
+        // Q fragments: 16 heads x 16 channels a step; rows past the group are zero.  FP8: channels 4 cq .. + 3 of the
+        // step, as its code words have them
+        const __nv_bfloat16 *qr = (const __nv_bfloat16 *)a.q + (int64_t)sg.b * a.ld_q + (int64_t)(g * G + h0) * DH;
+        auto load_q = [&](int k, uint32_t *f) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int h = gr + 8 * half;
-#pragma unroll
-                for (int k = 0; k < NK; ++k) {
-                    if constexpr (FP8) {   // channels 4 cq .. + 3 of the step: (0, 2) then (1, 3)
-                        uint2 w = make_uint2(0, 0);
-                        if (h < heads) w = __ldg(reinterpret_cast<const uint2 *>(qr + h * DH + 16 * k + 4 * cq));
-                        q[k][half] = __byte_perm(w.x, w.y, 0x5410);
-                        q[k][2 + half] = __byte_perm(w.x, w.y, 0x7632);
-                    } else {
-                        q[k][half] = q[k][2 + half] = 0;
-                        if (h < heads) {
-                            q[k][half] = __ldg(reinterpret_cast<const uint32_t *>(qr + h * DH + 16 * k + 2 * cq));
-                            q[k][2 + half] = __ldg(reinterpret_cast<const uint32_t *>(qr + h * DH + 16 * k + 8 + 2 * cq));
-                        }
-                    }
+                f[half] = f[2 + half] = 0;
+                if (h >= heads) continue;
+                if constexpr (FP8) {
+                    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(qr + h * DH + 16 * k + 4 * cq));
+                    f[half] = w.x;
+                    f[2 + half] = w.y;
+                } else {
+                    f[half] = __ldg(reinterpret_cast<const uint32_t *>(qr + h * DH + 16 * k + 2 * cq));
+                    f[2 + half] = __ldg(reinterpret_cast<const uint32_t *>(qr + h * DH + 16 * k + 8 + 2 * cq));
                 }
             }
+        };
+        uint32_t q[NK][4];
+#pragma unroll
+        for (int k = 0; k < NK; ++k) load_q(k, q[k]);
+        // FP8: to fp16 times 2^-up, the largest channel of a head in [2^14, 2^15)
+        int up0 = 0, up1 = 0;
+        bool q16 = false;
+        if constexpr (FP8) {
+            uint32_t big[2] = {0, 0};   // magnitude bits of bf16 order like the numbers
+#pragma unroll
+            for (int k = 0; k < NK; ++k)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    big[x & 1] = max(big[x & 1], max(q[k][x] & 0x7FFFu, (q[k][x] >> 16) & 0x7FFFu));
+#pragma unroll
+            for (int x = 1; x < 4; x <<= 1) {
+                big[0] = max(big[0], __shfl_xor_sync(0xffffffffu, big[0], x));
+                big[1] = max(big[1], __shfl_xor_sync(0xffffffffu, big[1], x));
+            }
+            q16 = big[0] < 0x7F80u && big[1] < 0x7F80u;   // finite
+            up0 = q16 && big[0] ? (int)(big[0] >> 7) - 127 - 14 : 0;
+            up1 = q16 && big[1] ? (int)(big[1] >> 7) - 127 - 14 : 0;
+            q16 = q16 && abs(up0) < 64 && abs(up1) < 64;
+#pragma unroll
+            for (int k = 0; k < NK; ++k)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float f = lp::pow2f(q16 ? -(x & 1 ? up1 : up0) : 0);
+                    const float lo = __uint_as_float(q[k][x] << 16) * f, hi = __uint_as_float(q[k][x] & 0xFFFF0000u) * f;
+                    const uint32_t r = pack2h(lo, hi);
+                    const __half2 back = *reinterpret_cast<const __half2 *>(&r);
+                    q16 = q16 && __low2float(back) == lo && __high2float(back) == hi;
+                    q[k][x] = r;
+                }
+            q16 = __all_sync(0xffffffffu, q16);
         }
+        int Ek = 0, Ev = -128;       // reference exponents (Ev: none yet)
         float o[2 * NK][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // heads gr and gr + 8
 #pragma unroll
         for (int i = 0; i < 2 * NK; ++i)
@@ -240,41 +283,70 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
             const int j0 = dk.token(sg.c0 + warp + i * kW);
             const bool whole = token_seen(dk, j0, a.sinks) && token_seen(dk, j0 + 15, a.sinks) &&
                                (j0 >= dk.w0 || j0 + 15 < a.sinks);
-            // the exponents of the four keys and two key columns this thread touches
-            uint32_t ke[2] = {0, 0}, ve[4] = {0, 0, 0, 0};
-            if constexpr (FP8) {
-                const uint8_t *ex = ring + (warp * NST + st) * Sh::kStage + 2 * Sh::kTile;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if constexpr (NB == 4) ke[t] = *reinterpret_cast<const uint32_t *>(ex + (gr + 8 * t) * 4);
-                    else ke[t] = *reinterpret_cast<const uint16_t *>(ex + (gr + 8 * t) * 2);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int row = 2 * cq + e + 8 * t;
-                        if constexpr (NB == 4) ve[2 * t + e] = *reinterpret_cast<const uint32_t *>(ex + Sh::kExps + row * 4);
-                        else ve[2 * t + e] = *reinterpret_cast<const uint16_t *>(ex + Sh::kExps + row * 2);
-                    }
-                }
-            }
-            if (!whole) {            // rows that are not seen: V to zero (FP8: codes and exponents)
+            if (!whole) {            // V rows that are not seen: zeros
                 for (int r = 0; r < 16; ++r) {
                     if (token_seen(dk, j0 + r, a.sinks)) continue;
                     uint8_t *v = ring + (warp * NST + st) * Sh::kStage + Sh::kTile;
                     if (lane < Sh::kTile / 256)
                         *reinterpret_cast<uint4 *>(v + tile_offset<DH, FP8>(r, lane)) = make_uint4(0, 0, 0, 0);
-                    if constexpr (FP8) {
-                        // exponents of K and V: the products of the zeros and of masked keys must not take the slow path
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (gr + 8 * t == r) ke[t] = 0;
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (2 * cq + e + 8 * t == r) ve[2 * t + e] = 0;
-                        }
-                    }
                 }
                 tc::fence_async_smem();   // ordered before the next TMA write of this stage
                 __syncwarp();
+            }
+            // FP8: the exponents of the K rows (gr, gr + 8) and V rows (2 cq, + 1, + 8, + 9) this thread touches; dk4, dv4:
+            // e - E + 8 by byte, in 0 .. 15 on the fast paths
+            uint32_t ke[2], ve[4], dk4[2], dv4[4];
+            bool k_fast = q16, v_fast = true;
+            if constexpr (FP8) {
+                const uint8_t *ex = ring + (warp * NST + st) * Sh::kStage + 2 * Sh::kTile;
+                auto word = [&](int r) -> uint32_t {   // unused bytes repeat used ones
+                    if constexpr (NB == 4) return *reinterpret_cast<const uint32_t *>(ex + r * 4);
+                    else return *reinterpret_cast<const uint16_t *>(ex + r * 2) * 0x00010001u;
+                };
+#pragma unroll
+                for (int t = 0; t < 2; ++t) ke[t] = word(gr + 8 * t);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) ve[t] = word(16 + 2 * cq + (t & 1) + 8 * (t >> 1));
+                uint32_t hide_k = 0, hide_v = 0;   // rows that are not seen
+                if (!whole) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        if (!token_seen(dk, j0 + gr + 8 * t, a.sinks)) hide_k |= 1u << t;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (!token_seen(dk, j0 + 2 * cq + (t & 1) + 8 * (t >> 1), a.sinks)) hide_v |= 1u << t;
+                }
+                auto offsets = [&](const uint32_t *e, uint32_t *d, int n, int E, uint32_t hide) {
+                    uint32_t out = 0;
+                    for (int t = 0; t < n; ++t) {
+                        d[t] = hide >> t & 1 ? 0x08080808u : __vsub4(e[t], (uint32_t)((E - 8) & 255) * 0x01010101u);
+                        out |= d[t];
+                    }
+                    return !__any_sync(0xffffffffu, out & 0xF0F0F0F0u);
+                };
+                auto largest = [&](const uint32_t *e, int n, uint32_t hide) {
+                    int m = -126;
+                    for (int t = 0; t < n; ++t)
+                        if (!(hide >> t & 1)) m = max(m, max4s(e[t]));
+                    return __reduce_max_sync(0xffffffffu, m);
+                };
+                if (k_fast && !offsets(ke, dk4, 2, Ek, hide_k)) {
+                    const int top = largest(ke, 2, hide_k);
+                    k_fast = abs(top) < 60 && offsets(ke, dk4, 2, top, hide_k);
+                    if (k_fast) Ek = top;
+                }
+                if (Ev == -128 || !offsets(ve, dv4, 4, Ev, hide_v)) {
+                    const int top = largest(ve, 4, hide_v);
+                    if (top > Ev) {
+                        const float f = pow2_or_0(Ev - top);   // no value yet: O is zero
+                        Ev = top;
+#pragma unroll
+                        for (int j = 0; j < 2 * NK; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[j][e] *= f;
+                    }
+                    v_fast = offsets(ve, dv4, 4, Ev, hide_v);
+                }
             }
             float sc[2][4], sd[2][4];   // even and odd steps: two shorter chains of products
 #pragma unroll
@@ -290,43 +362,45 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                     mma16816(k & 1 ? sd[1] : sc[1], q[k], b[2], b[3]);
                 }
             } else {
-                uint32_t w[NK / 2][4], nan = 0;
-#pragma unroll
-                for (int k = 0; k < NK / 2; ++k) {
-                    ldsm4(kt + tile_offset<DH, FP8>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4)), w[k]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) nan |= nan_bits(w[k][e]);
-                }
-                if (!__any_sync(0xffffffffu, (nan | big_bits(ke[0]) | big_bits(ke[1])) & 0x80808080u)) {
-                    const uint32_t z[2] = {fields(ke[0]), fields(ke[1])};
+                if (k_fast) {
+                    const uint32_t z[2] = {dk4[0] + 0x07070707u, dk4[1] + 0x07070707u};   // fp16 exponent fields
 #pragma unroll
                     for (int k = 0; k < NK / 2; ++k) {   // steps 2 k and 2 k + 1: block k
+                        uint32_t w[4];
+                        ldsm4(kt + tile_offset<DH, FP8>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4)), w);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint32_t b0, b1;
-                            // byte k of z in both halves, in the place of a bf16 exponent
-                            codes_fast(w[k][e], __byte_perm(z[e & 1], 0, 0x4040 + 0x0101 * k) << 7, b0, b1);
-                            mma16816(e >> 1 ? sd[e & 1] : sc[e & 1], q[2 * k + (e >> 1)], b0, b1);
+                            // byte k of z in both halves
+                            const uint32_t f = __byte_perm(z[e & 1], 0, 0x4040 + 0x0101 * k) << 10;
+                            codes_f16(w[e], f, f, b0, b1);
+                            mma16816h(e >> 1 ? sd[e & 1] : sc[e & 1], q[2 * k + (e >> 1)], b0, b1);
                         }
                     }
                 } else {
 #pragma unroll
                     for (int k = 0; k < NK / 2; ++k) {
+                        uint32_t w[4], qb[2][4];
+                        ldsm4(kt + tile_offset<DH, FP8>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4)), w);
+                        load_q(2 * k, qb[0]);
+                        load_q(2 * k + 1, qb[1]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint32_t b0, b1;
                             const float f = lp::pow2f((int8_t)(ke[e & 1] >> (8 * k)));
-                            codes_any(w[k][e], f, f, b0, b1);
-                            mma16816(e >> 1 ? sd[e & 1] : sc[e & 1], q[2 * k + (e >> 1)], b0, b1);
+                            codes_bf16(w[e], f, f, f, f, b0, b1);
+                            mma16816(e >> 1 ? sd[e & 1] : sc[e & 1], qb[e >> 1], b0, b1);
                         }
                     }
                 }
             }
+            const bool scaled = FP8 && k_fast;   // undo the scales of Q and K
+            const float s0 = scaled ? scale * lp::pow2f(up0 + Ek) : scale, s1 = scaled ? scale * lp::pow2f(up1 + Ek) : scale;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    sc[t][e] = (sc[t][e] + sd[t][e]) * scale;
+                    sc[t][e] = (sc[t][e] + sd[t][e]) * (e < 2 ? s0 : s1);
                     if (!whole && !token_seen(dk, j0 + 8 * t + 2 * cq + (e & 1), a.sinks)) sc[t][e] = -INFINITY;
                 }
             float n0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
@@ -353,7 +427,8 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                     o[j][3] *= f1;
                 }
             }
-            const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
+            constexpr float kUp = FP8 ? 15.f : 0.f;   // weights times 2^kUp
+            const float r0 = m0 == -INFINITY ? 0.f : m0 - kUp, r1 = m1 == -INFINITY ? 0.f : m1 - kUp;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 sc[t][0] = ex2(sc[t][0] - r0);
@@ -363,8 +438,14 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                 l0 += sc[t][0] + sc[t][1];
                 l1 += sc[t][2] + sc[t][3];
             }
-            const uint32_t p[4] = {pack2(sc[0][0], sc[0][1]), pack2(sc[0][2], sc[0][3]), pack2(sc[1][0], sc[1][1]),
-                                   pack2(sc[1][2], sc[1][3])};
+            uint32_t p[4];
+            if (FP8 && v_fast) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) p[t] = pack2h(sc[t >> 1][2 * (t & 1)], sc[t >> 1][2 * (t & 1) + 1]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) p[t] = pack2(sc[t >> 1][2 * (t & 1)], sc[t >> 1][2 * (t & 1) + 1]);
+            }
             if constexpr (!FP8) {
 #pragma unroll
                 for (int j = 0; j < NK; ++j) {
@@ -374,44 +455,44 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                     mma16816(o[2 * j + 1], p, b[2], b[3]);
                 }
             } else {
-                uint32_t w[NK / 2][4], nan = 0;
-#pragma unroll
-                for (int j = 0; j < NK / 2; ++j) {
-                    ldsm4t(vt + tile_offset<DH, FP8>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * j + (lane >> 4)), w[j]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) nan |= nan_bits(w[j][e]);
-                }
-#pragma unroll
-                for (int t = 0; t < 4; ++t) nan |= big_bits(ve[t]);
-                // granules 2 j and 2 j + 1 of the row: block j; t: keys 0..7, 8..15
-                if (!__any_sync(0xffffffffu, nan & 0x80808080u)) {
-                    const uint32_t z[4] = {fields(ve[0]), fields(ve[1]), fields(ve[2]), fields(ve[3])};
+                // granules 2 j and 2 j + 1 of the row: block j.  A word of ldmatrix.trans: two channels of key 2 cq, then the
+                // same of key 2 cq + 1 (t: keys 0..7, 8..15)
+                if (v_fast) {
 #pragma unroll
                     for (int j = 0; j < NK / 2; ++j) {
-                        uint32_t f[2];
+                        uint32_t w[4], f[2];
+                        ldsm4t(vt + tile_offset<DH, FP8>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * j + (lane >> 4)), w);
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) f[t] = (__byte_perm(z[2 * t], z[2 * t + 1], 0x0400 + 0x0101 * j) & 0x00FF00FFu) << 7;
+                        for (int t = 0; t < 2; ++t)
+                            f[t] = ((__byte_perm(dv4[2 * t], dv4[2 * t + 1], 0x0400 + 0x0101 * j) & 0x000F000Fu) +
+                                    0x00070007u) << 10;
 #pragma unroll
                         for (int gi = 0; gi < 2; ++gi) {
-                            uint32_t e0[2], o0[2];
+                            uint32_t c0[2], c1[2];
 #pragma unroll
-                            for (int t = 0; t < 2; ++t) codes_fast(w[j][2 * gi + t], f[t], e0[t], o0[t]);
-                            mma16816(o[2 * (2 * j + gi)], p, e0[0], e0[1]);
-                            mma16816(o[2 * (2 * j + gi) + 1], p, o0[0], o0[1]);
+                            for (int t = 0; t < 2; ++t)
+                                codes_f16(__byte_perm(w[2 * gi + t], 0, 0x3120), f[t], f[t], c0[t], c1[t]);
+                            mma16816h(o[2 * (2 * j + gi)], p, c0[0], c0[1]);
+                            mma16816h(o[2 * (2 * j + gi) + 1], p, c1[0], c1[1]);
                         }
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < NK / 2; ++j) {
+                        uint32_t w[4];
+                        ldsm4t(vt + tile_offset<DH, FP8>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * j + (lane >> 4)), w);
 #pragma unroll
                         for (int gi = 0; gi < 2; ++gi) {
-                            uint32_t e0[2], o0[2];
+                            uint32_t c0[2], c1[2];
 #pragma unroll
-                            for (int t = 0; t < 2; ++t)
-                                codes_any(w[j][2 * gi + t], lp::pow2f((int8_t)(ve[2 * t] >> (8 * j))),
-                                          lp::pow2f((int8_t)(ve[2 * t + 1] >> (8 * j))), e0[t], o0[t]);
-                            mma16816(o[2 * (2 * j + gi)], p, e0[0], e0[1]);
-                            mma16816(o[2 * (2 * j + gi) + 1], p, o0[0], o0[1]);
+                            for (int t = 0; t < 2; ++t) {
+                                // a row that is not seen has codes 0; its exponent may be anything
+                                const float fa = pow2_or_0(min((int8_t)(ve[2 * t] >> (8 * j)) - Ev, 127));
+                                const float fb = pow2_or_0(min((int8_t)(ve[2 * t + 1] >> (8 * j)) - Ev, 127));
+                                codes_bf16(__byte_perm(w[2 * gi + t], 0, 0x3120), fa, fb, fa, fb, c0[t], c1[t]);
+                            }
+                            mma16816(o[2 * (2 * j + gi)], p, c0[0], c0[1]);
+                            mma16816(o[2 * (2 * j + gi) + 1], p, c1[0], c1[1]);
                         }
                     }
                 }
@@ -425,6 +506,15 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
         l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+        if constexpr (FP8) {         // undo the weights' and V's references
+            const float f = pow2_or_0(Ev);
+            l0 *= 0x1p-15f;
+            l1 *= 0x1p-15f;
+#pragma unroll
+            for (int j = 0; j < 2 * NK; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[j][e] = o[j][e] * 0x1p-15f * f;
+        }
         if (cq == 0) {
             sm_m[warp][gr] = m0;
             sm_m[warp][gr + 8] = m1;

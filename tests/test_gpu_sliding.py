@@ -599,3 +599,36 @@ def test_prefill_then_decode_through_the_layers(h, lowprec):
             # bf16 (2^-7) of values near 1, averaged by the projections
             assert ((x[1].float() - full[t].float()).abs().max() <= 2.0 ** -4)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("what", ["spread", "rising", "falling", "wide query", "huge", "tiny"])
+def test_decode_fp8_exponents(h, dh, what):
+    """FP8 pages whose blocks' exponents differ by far more than fp16 spans, rise or fall along the sequence, or lie at the
+    ends of the range; a query whose channels span more than fp16 does."""
+    n, H, Hkv = 700, 16, 2
+    c = Paged(h, [n - 1, 130], H, Hkv, dh, NO_WINDOW, 0, 32, "bf16", True, seed=17)
+    g = gen(18)
+    k, v = randn(g, n, Hkv * dh), randn(g, n, Hkv * dh)
+    step = torch.arange(n, device="cuda")[:, None]
+    if what == "spread":         # value blocks 2^-40 .. 2^30 next to each other, keys 2^-20 .. 1
+        v = v * torch.exp2(((step * 7 + torch.arange(Hkv * dh, device="cuda") // 32 * 13) % 71 - 40).float()).to(v.dtype)
+        k = k * torch.exp2(-((step * 5) % 21).float()).to(k.dtype)
+    elif what == "rising":
+        v = v * torch.exp2((step // 10 - 30).float()).to(v.dtype)
+        k = k * torch.exp2((step // 100 - 6).float()).to(k.dtype)
+    elif what == "falling":
+        v = v * torch.exp2((30 - step // 10).float()).to(v.dtype)
+        k = k * torch.exp2((-(step // 50)).float()).to(k.dtype)
+    elif what == "wide query":
+        c.q = c.q * torch.exp2((torch.arange(H * dh, device="cuda") % 50 - 49).float()).to(c.q.dtype)
+    elif what == "huge":
+        v = v * 2.0 ** 100
+        k, c.q = k * 2.0 ** 90, c.q * 2.0 ** -90
+    else:
+        v = v * 2.0 ** -100
+        k, c.q = k * 2.0 ** -90, c.q * 2.0 ** 90
+    at = torch.arange(n, dtype=torch.int32, device="cuda")
+    for b, x in enumerate(c.pos_h):
+        h.swa_page_append(c.p, c.pages, at[:x + 1], k[:x + 1], v[:x + 1], torch.full_like(at[:x + 1], b))
+    c.check(c.decode())
