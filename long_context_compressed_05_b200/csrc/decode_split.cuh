@@ -1,18 +1,18 @@
 // How a decode step over ragged paged sequences is split over CTAs, shared by its kernels.
 //
-// A unit is (sequence, key head, block of query heads); its work is the sequence's chunks of 16 tokens.  All
+// A unit is (sequence, key head, block of query heads); its work is the sequence's chunks of CT (16 or 32) tokens.  All
 // units' chunks in order form one list that the CTAs share out in equal contiguous pieces, whatever the
 // sequences' lengths; a CTA walks its piece unit by unit (segments).  A unit inside one piece is finished by
 // its CTA; the others leave one partial per CTA (at most the piece's first and last segment: two slots), and
 // a second kernel joins them in CTA order, so the result does not depend on timing.  Where no unit can have
-// more than kDirectChunks chunks (a short window), every CTA takes one whole unit and nothing is joined.
+// more than kDirectTokens tokens (a short window), every CTA takes one whole unit and nothing is joined.
 #pragma once
 
 #include "sliding.cuh"
 
 namespace hcsa {
 
-constexpr int kDirectChunks = 16;   // 256 tokens
+constexpr int kDirectTokens = 256;
 constexpr int kMinShare = 8;        // chunks: a smaller piece costs more to join than it saves
 
 struct Split {
@@ -63,7 +63,7 @@ struct Piece {
     int b;
     int64_t off, len;
 };
-template <int NT>
+template <int NT, int CT>
 __device__ __forceinline__ Piece piece_of(const DecodeArgs &a, const Split &s, int64_t *sh) {
     __shared__ int sh_b;
     __shared__ int64_t sh_off;
@@ -71,7 +71,7 @@ __device__ __forceinline__ Piece piece_of(const DecodeArgs &a, const Split &s, i
     for (int base = 0; base < a.c.B; base += NT) {
         const int b = base + threadIdx.x;
         const int64_t v =
-            b < a.c.B ? (int64_t)decode_keys(a.pos[b], a.window, a.sinks, capacity_of(a), a.c.status).n * s.units_per_seq : 0;
+            b < a.c.B ? (int64_t)decode_keys<CT>(a.pos[b], a.window, a.sinks, capacity_of(a), a.c.status).n * s.units_per_seq : 0;
         const int64_t incl = block_scan<NT>(v, &all, sh);
         if (blockIdx.x == 0 && b < a.c.B) s.prefix[b] = total + incl - v;
         total += all;
@@ -85,7 +85,7 @@ __device__ __forceinline__ Piece piece_of(const DecodeArgs &a, const Split &s, i
     for (int base = 0; base < a.c.B && run <= start; base += NT) {
         const int b = base + threadIdx.x;
         const int64_t v =
-            b < a.c.B ? (int64_t)decode_keys(a.pos[b], a.window, a.sinks, capacity_of(a), nullptr).n * s.units_per_seq : 0;
+            b < a.c.B ? (int64_t)decode_keys<CT>(a.pos[b], a.window, a.sinks, capacity_of(a), nullptr).n * s.units_per_seq : 0;
         const int64_t incl = run + block_scan<NT>(v, &all, sh);
         if (incl - v <= start && start < incl) {
             sh_b = b;
@@ -101,7 +101,7 @@ __device__ __forceinline__ Piece piece_of(const DecodeArgs &a, const Split &s, i
 
 size_t decode_split_bytes(int B, int grid, int heads, int dh);
 Split make_split(const DecodeArgs &a, int units_per_seq, int heads, int grid);
-int decode_grid();                  // CTAs of a split step
+int decode_grid(int per_sm);        // CTAs of a split step
 // zero rows of empty slots and join the partials; heads: query heads per unit, blocks: head blocks per key head
 hcsa_status launch_decode_join(const DecodeArgs &a, const Split &s, int heads, int grid, cudaStream_t st);
 bool decode_direct(const DecodeArgs &a);
@@ -110,6 +110,7 @@ hcsa_status launch_decode_simt(const DecodeArgs &a, cudaStream_t st);
 int decode_simt_heads(int dh);
 bool decode_tc_supported(int dtype, int dh);
 int decode_tc_heads();
+int decode_tc_grid();
 hcsa_status launch_decode_tc(const DecodeArgs &a, cudaStream_t st);
 
 }  // namespace hcsa

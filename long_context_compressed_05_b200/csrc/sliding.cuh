@@ -126,8 +126,6 @@ __device__ void attend_row(const SwaArgs &a, int t, int h, int lane) {
 }
 
 // ---------------------------------------------------------------- paged cache
-constexpr int kChunk16 = 16;               // tokens per chunk; a chunk never crosses a page
-
 struct PageArgs {
     int dtype;
     bool lowprec;
@@ -151,28 +149,33 @@ struct DecodeArgs {
 size_t swa_decode_ws_bytes(int dtype, int B, int dh);
 hcsa_status launch_swa_decode(const DecodeArgs &a, cudaStream_t st);
 
-// Chunks of 16 tokens that the new token of a sequence reads: those of the first tokens, then those from
-// the window's first chunk on (from token 0 when the two meet).
+// Chunks of CT tokens (aligned, and CT divides the page: a chunk never crosses one) that the new token of a
+// sequence reads: those of the first tokens, then those from the window's first chunk on (from token 0 when
+// the two meet).
+template <int CT>
 struct DecodeKeys {
     int pos, w0, n_far, far_end, n;        // far_end: token of chunk n_far (the window's first chunk)
-    __device__ __forceinline__ int token(int c) const { return c < n_far ? 16 * c : far_end + 16 * (c - n_far); }
+    __device__ __forceinline__ int token(int c) const { return c < n_far ? CT * c : far_end + CT * (c - n_far); }
+    __device__ __forceinline__ bool seen(int j, int sinks) const { return j <= pos && (j >= w0 || j < sinks); }
+    // every token of the chunk that starts at j
+    __device__ __forceinline__ bool all_seen(int j, int sinks) const {
+        return j + CT - 1 <= pos && (j >= w0 || j + CT <= sinks);
+    }
 };
-__device__ __forceinline__ DecodeKeys decode_keys(int pos, int window, int sinks, int64_t capacity, int *status) {
-    DecodeKeys k{pos, 0, 0, 0, 0};
+template <int CT>
+__device__ __forceinline__ DecodeKeys<CT> decode_keys(int pos, int window, int sinks, int64_t capacity, int *status) {
+    DecodeKeys<CT> k{pos, 0, 0, 0, 0};
     if (pos < 0) return k;
     if (pos >= capacity) {
         report(status, kStatusBounds);
         return k;
     }
     k.w0 = pos - window + 1 > 0 ? pos - window + 1 : 0;
-    k.far_end = k.w0 & ~15;
-    k.n_far = ((sinks < k.w0 ? sinks : k.w0) + 15) >> 4;
-    if (16 * k.n_far >= k.far_end) k.n_far = k.far_end = 0;
-    k.n = k.n_far + ((pos - k.far_end) >> 4) + 1;
+    k.far_end = k.w0 / CT * CT;
+    k.n_far = ((sinks < k.w0 ? sinks : k.w0) + CT - 1) / CT;
+    if (CT * k.n_far >= k.far_end) k.n_far = k.far_end = 0;
+    k.n = k.n_far + (pos - k.far_end) / CT + 1;
     return k;
-}
-__device__ __forceinline__ bool token_seen(const DecodeKeys &k, int j, int sinks) {
-    return j <= k.pos && (j >= k.w0 || j < sinks);
 }
 
 // Exponent of a 32-channel block in the pages and the norm's output: the smallest e with

@@ -13,6 +13,7 @@ namespace hcsa {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kPerSM = 2;            // CTAs per SM of a split step
 
 template <int DH> constexpr int heads_of() { return DH <= 256 ? 8 : 2; }
 
@@ -74,11 +75,11 @@ __global__ void __launch_bounds__(32 * kWarps) swa_decode_simt_kernel(DecodeArgs
         pc.off = 0;
         pc.len = 1;
     } else {
-        pc = piece_of<32 * kWarps>(a, s, sh);
+        pc = piece_of<32 * kWarps, 16>(a, s, sh);
     }
     int64_t done = 0;
     while (done < pc.len) {
-        const DecodeKeys dk = decode_keys(a.pos[pc.b], a.window, a.sinks, capacity_of(a), a.c.status);
+        const DecodeKeys<16> dk = decode_keys<16>(a.pos[pc.b], a.window, a.sinks, capacity_of(a), a.c.status);
         Segment sg;
         sg.b = pc.b;
         sg.n = dk.n;
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(32 * kWarps) swa_decode_simt_kernel(DecodeArgs
             for (int t = 0; t < 16; t += 4) {
                 bool any = false;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) any = any || token_seen(dk, j0 + t + i, a.sinks);
+                for (int i = 0; i < 4; ++i) any = any || dk.seen(j0 + t + i, a.sinks);
                 if (!any) continue;
                 float k[4][N], v[4][N];
 #pragma unroll
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(32 * kWarps) swa_decode_simt_kernel(DecodeArgs
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     // a row that is not seen is not read: it may hold anything
-                    if (token_seen(dk, j0 + t + i, a.sinks)) load_row<S, FP8, DH>(a, a.c.v_pages, line + t + i, lane, v[i]);
+                    if (dk.seen(j0 + t + i, a.sinks)) load_row<S, FP8, DH>(a, a.c.v_pages, line + t + i, lane, v[i]);
                     else
 #pragma unroll
                         for (int e = 0; e < N; ++e) v[i][e] = 0.f;
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(32 * kWarps) swa_decode_simt_kernel(DecodeArgs
                     }
                 }
                 for (; o; o >>= 1) r[0] += __shfl_xor_sync(0xffffffffu, r[0], o);
-                const float sc = token_seen(dk, j0 + t + kg, a.sinks) ? r[0] : -INFINITY;
+                const float sc = dk.seen(j0 + t + kg, a.sinks) ? r[0] : -INFINITY;
                 float mn = fmaxf(m, sc);   // of the head: its four lanes differ in the two upper bits
                 mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 16));
                 mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 8));
@@ -230,51 +231,89 @@ __global__ void __launch_bounds__(32 * kWarps) swa_decode_simt_kernel(DecodeArgs
     }
 }
 
-// Joins the partials of one (unit, head): blocks of 128 threads, warps take every fourth partial, lanes the
-// dims; empty slots get their zeros here.
-template <typename S>
-__global__ void __launch_bounds__(128) decode_join_kernel(DecodeArgs a, Split s, int HB, int grid) {
+// Joins the partials of one (unit, head) per block; empty slots get their zeros here.  Bound by the latency of its
+// three dependent reads (prefix, (max, sum) pairs, O rows), so all of a read's loads are issued together: the
+// pairs by all threads, then each warp takes every eighth row, kRows of them at a time.
+constexpr int kJoinWarps = 8, kMaxParts = 2048;
+template <typename S, int N>   // N: dims per lane (of dh <= 32 N)
+__global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(DecodeArgs a, Split s, int HB, int grid) {
+    constexpr int kRows = N <= 4 ? 8 : 2;
     const int G = a.H / a.c.Hkv, blocks = (G + HB - 1) / HB;
     const int b = blockIdx.x / a.H, hq = blockIdx.x % a.H, g = hq / G, hg = hq % G;
     const int u = g * blocks + hg / HB, h = hg % HB;
-    const int64_t p0 = s.prefix[b], n = (s.prefix[b + 1] - p0) / s.units_per_seq;
+    const int64_t p0 = s.prefix[b], n = (s.prefix[b + 1] - p0) / s.units_per_seq, total = s.prefix[a.c.B];
     S *dst = (S *)a.out + (int64_t)b * a.ld_out + (int64_t)hq * a.c.dh;
     if (n == 0) {
-        for (int d = threadIdx.x; d < a.c.dh; d += 128) store_val(dst + d, 0.f);
+        for (int d = threadIdx.x; d < a.c.dh; d += 32 * kJoinWarps) store_val(dst + d, 0.f);
         return;
     }
-    const int64_t share = share_of(s.prefix[a.c.B], grid), t0 = p0 + u * n;
-    const int first = (int)(t0 / share), last = (int)((t0 + n - 1) / share);
-    if (first == last) return;   // finished by its CTA
+    const int64_t share = share_of(total, grid), t0 = p0 + u * n;
+    const int first = (int)(t0 / share), last = (int)((t0 + n - 1) / share), parts = last - first + 1;
+    if (parts == 1) return;   // finished by its CTA
     const bool late = t0 % share != 0;   // the unit starts inside its first CTA's piece: second slot
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto at = [&](int c) { return ((int64_t)c * 2 + (c == first && late ? 1 : 0)) * HB + h; };
-    __shared__ float sm_x[4][512], sm_l[4];
+    auto at = [&](int i) { return ((int64_t)(first + i) * 2 + (i == 0 && late ? 1 : 0)) * HB + h; };
+    __shared__ float sm_f[kMaxParts], sm_m[kJoinWarps], sm_l[kJoinWarps];   // parts <= grid <= kMaxParts
+    __shared__ float sm_x[kJoinWarps][32 * N];
     float m = -INFINITY;
-    for (int c = first + lane; c <= last; c += 32) m = fmaxf(m, s.ml[2 * at(c)]);
+    float2 ml[kMaxParts / (32 * kJoinWarps)];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f, x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.f;
-#pragma unroll 4
-    for (int c = first + warp; c <= last; c += 4) {
-        const int64_t i = at(c);
-        const float mc = s.ml[2 * i], f = mc == -INFINITY ? 0.f : exp2f(mc - ref);
-        l += s.ml[2 * i + 1] * f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (32 * e < a.c.dh && lane + 32 * e < a.c.dh) x[e] += s.acc[i * a.c.dh + lane + 32 * e] * f;
+    for (int i = 0; i < kMaxParts / (32 * kJoinWarps); ++i) {
+        const int c = i * 32 * kJoinWarps + threadIdx.x;
+        ml[i] = c < parts ? *reinterpret_cast<const float2 *>(s.ml + 2 * at(c)) : make_float2(-INFINITY, 0.f);
+        m = fmaxf(m, ml[i].x);
     }
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-        if (32 * e < a.c.dh) sm_x[warp][lane + 32 * e] = x[e];
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) sm_m[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sm_m[w]);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxParts / (32 * kJoinWarps); ++i) {
+        const int c = i * 32 * kJoinWarps + threadIdx.x;
+        if (c >= parts) break;
+        const float f = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - ref);
+        sm_f[c] = f;
+        l += ml[i].y * f;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) sm_l[warp] = l;
     __syncthreads();
-    l = sm_l[0] + sm_l[1] + sm_l[2] + sm_l[3];
-    for (int d = threadIdx.x; d < a.c.dh; d += 128)
-        store_val(dst + d, (sm_x[0][d] + sm_x[1][d] + sm_x[2][d] + sm_x[3][d]) / l);
+    float x[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = 0.f;
+    for (int c0 = warp; c0 < parts; c0 += kJoinWarps * kRows) {
+        float v[kRows][N];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int c = c0 + r * kJoinWarps;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                v[r][e] = c < parts && lane + 32 * e < a.c.dh ? s.acc[at(c) * a.c.dh + lane + 32 * e] : 0.f;
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const float f = c0 + r * kJoinWarps < parts ? sm_f[c0 + r * kJoinWarps] : 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[e] += v[r][e] * f;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) sm_x[warp][lane + 32 * e] = x[e];
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) l += sm_l[w];
+    for (int d = threadIdx.x; d < a.c.dh; d += 32 * kJoinWarps) {
+        float y = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) y += sm_x[w][d];
+        store_val(dst + d, y / l);
+    }
 }
 
 template <typename S, bool FP8, int DH>
@@ -286,7 +325,7 @@ hcsa_status launch_simt(const DecodeArgs &a, cudaStream_t st) {
     const int G = a.H / a.c.Hkv, units = a.c.Hkv * ((G + HB - 1) / HB);
     const bool direct = decode_direct(a);
     if (direct && (int64_t)a.c.B * units > INT32_MAX) return HCSA_ERR_UNSUPPORTED;
-    const int grid = direct ? a.c.B * units : decode_grid();
+    const int grid = direct ? a.c.B * units : decode_grid(kPerSM);
     Split s = make_split(a, units, HB, grid);
     s.direct = direct;
     swa_decode_simt_kernel<S, FP8, DH><<<grid, 32 * kWarps, smem, st>>>(a, s);
@@ -309,18 +348,18 @@ size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 int decode_simt_heads(int dh) { return dh <= 256 ? 8 : 2; }
 
-int decode_grid() {
+int decode_grid(int per_sm) {
     static int n[64] = {};
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
     if (!n[dev]) {
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
             cudaGetLastError();
-            return 2 * 148;
+            return per_sm * 148;
         }
-        n[dev] = 2 * sms;
+        n[dev] = sms;
     }
-    return n[dev];
+    return per_sm * n[dev];
 }
 
 size_t decode_split_bytes(int B, int grid, int heads, int dh) {
@@ -340,17 +379,24 @@ Split make_split(const DecodeArgs &a, int units_per_seq, int heads, int grid) {
     return s;
 }
 
-// No unit has more than kDirectChunks chunks: the window's (one more where it starts inside a chunk) and the sinks'.
+// No unit reads more than kDirectTokens: the window's tokens and the first ones, in whole chunks of 16.
 bool decode_direct(const DecodeArgs &a) {
-    const int64_t cap = (int64_t)a.c.max_pages * a.c.page / 16;
-    const int64_t seen = ((int64_t)a.window + 15) / 16 + 1 + ((int64_t)a.sinks + 15) / 16;
-    return (cap < seen ? cap : seen) <= kDirectChunks;
+    const int64_t cap = (int64_t)a.c.max_pages * a.c.page;
+    const int64_t seen = ((int64_t)a.window + 30) / 16 * 16 + ((int64_t)a.sinks + 15) / 16 * 16;
+    return (cap < seen ? cap : seen) <= kDirectTokens;
 }
 
 hcsa_status launch_decode_join(const DecodeArgs &a, const Split &s, int heads, int grid, cudaStream_t st) {
-    if ((int64_t)a.c.B * a.H > INT32_MAX) return HCSA_ERR_UNSUPPORTED;
-    if (a.c.dtype == HCSA_F32) decode_join_kernel<float><<<a.c.B * a.H, 128, 0, st>>>(a, s, heads, grid);
-    else decode_join_kernel<__nv_bfloat16><<<a.c.B * a.H, 128, 0, st>>>(a, s, heads, grid);
+    if ((int64_t)a.c.B * a.H > INT32_MAX || grid > kMaxParts) return HCSA_ERR_UNSUPPORTED;
+    const unsigned n = (unsigned)(a.c.B * a.H), t = 32 * kJoinWarps;
+    auto run = [&](auto one) {
+        using S = decltype(one);
+        if (a.c.dh <= 64) decode_join_kernel<S, 2><<<n, t, 0, st>>>(a, s, heads, grid);
+        else if (a.c.dh <= 128) decode_join_kernel<S, 4><<<n, t, 0, st>>>(a, s, heads, grid);
+        else decode_join_kernel<S, 16><<<n, t, 0, st>>>(a, s, heads, grid);
+    };
+    if (a.c.dtype == HCSA_F32) run(float());
+    else run(__nv_bfloat16());
     count_launch();
     return check_launch();
 }
@@ -361,8 +407,8 @@ hcsa_status launch_decode_simt(const DecodeArgs &a, cudaStream_t st) {
 }
 
 size_t swa_decode_ws_bytes(int dtype, int B, int dh) {
-    const int heads = decode_tc_supported(dtype, dh) ? decode_tc_heads() : decode_simt_heads(dh);
-    return decode_split_bytes(B, decode_grid(), heads, dh);
+    return decode_tc_supported(dtype, dh) ? decode_split_bytes(B, decode_tc_grid(), decode_tc_heads(), dh)
+                                          : decode_split_bytes(B, decode_grid(kPerSM), decode_simt_heads(dh), dh);
 }
 
 hcsa_status launch_swa_decode(const DecodeArgs &a, cudaStream_t st) {

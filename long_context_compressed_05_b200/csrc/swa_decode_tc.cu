@@ -20,8 +20,8 @@
 // picked again for a chunk that leaves the range; the V reference (O is held times 2^-E) is raised with O rescaled;
 // a chunk whose exponents spread further takes the slow path: bf16 operands by full conversions.  Queries are scaled
 // per head to fp16 by a power of two where that is exact (a ratio of 2^32 between the largest and the smallest
-// channel), else the segment takes the slow path.  Weights are held times 2^15, so their rounding to fp16 is
-// relative (2^-11) down to 2^-29 of the largest.  Codes 2i and 2i + 1 of a word share a register (K), or two keys'
+// channel), else the segment takes the slow path.  Weights are held times 2^11, so their rounding to fp16 is
+// relative (2^-11) down to 2^-25 of the largest.  Codes 2i and 2i + 1 of a word share a register (K), or two keys'
 // codes of one channel (V), so channels run in a permuted order that the Q fragments and the stores follow.
 #include "decode_split.cuh"
 #include "tc_common.cuh"
@@ -34,16 +34,17 @@ namespace {
 
 constexpr int kW = 4;                // warps
 constexpr int kHB = 16;              // query heads of a unit
-constexpr int kRingBytes = 104 * 1024;   // two CTAs per SM
+constexpr int kPerSM = 3;            // CTAs per SM: the step's dependent latencies need about twelve warps
+constexpr int kRingBytes = 70 * 1024;
 
-template <int DH, bool FP8> struct Shape {
-    static constexpr int kTile = 16 * DH * (FP8 ? 1 : 2);          // K or V of a chunk
-    static constexpr int kExps = FP8 ? 16 * (DH / 32) : 0;
-    static constexpr int kStage = (2 * kTile + 2 * kExps + 1023) / 1024 * 1024;
+// CT: tokens per chunk.  FP8 chunks are 32 where the pages allow it: a step's instructions that do not grow with the
+// chunk (waits, masks, maxima, page lines) were half of its issue slots at 16 (104 -> 86 us at 8 sequences up to 262144).
+template <int DH, bool FP8, int CT> struct Shape {
+    static constexpr int kTile = CT * DH * (FP8 ? 1 : 2);          // K or V of a chunk
+    static constexpr int kStage = 2 * kTile;
     static constexpr int kStages = kRingBytes / (kW * kStage) < 8 ? kRingBytes / (kW * kStage) : 8;
-    static constexpr int kTx = 2 * kTile + 2 * kExps;
     static constexpr int kSmem = kW * kStages * kStage + 1024;
-    static_assert(kW * kHB * DH * 4 <= kW * kStages * kStage, "the join fits in the ring");
+    static_assert(kStages >= 2 && kW * kHB * DH * 4 <= kW * kStages * kStage, "the join fits in the ring");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -112,21 +113,21 @@ __device__ __forceinline__ int max4s(uint32_t e) {   // largest of four signed b
 __device__ __forceinline__ float pow2_or_0(int e) { return e < -126 ? 0.f : lp::pow2f(e); }
 
 // byte offset of granule g (16 bytes) of row r in a K or V tile, as the TMA box leaves it
-template <int DH, bool FP8>
+template <int DH, bool FP8, int CT>
 __device__ __forceinline__ uint32_t tile_offset(int r, int g) {
     if constexpr (FP8 && DH == 64) {          // 64-byte rows, 64-byte swizzle
         return r * 64 + ((g ^ ((r >> 1) & 3)) << 4);
     } else {                                  // 128-byte rows, 128-byte swizzle; bf16 dh 128: two such halves
-        return (g >> 3) * 2048 + tc::sw128_offset(r, g & 7);
+        return (g >> 3) * (CT * 128) + tc::sw128_offset(r, g & 7);
     }
 }
 
-template <int DH, bool FP8>
-__global__ void __launch_bounds__(32 * kW, 2)
+template <int DH, bool FP8, int CT>
+__global__ void __launch_bounds__(32 * kW, kPerSM)
 swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v) {
-    using Sh = Shape<DH, FP8>;
-    constexpr int NST = Sh::kStages, NK = DH / 16, NB = DH / 32;
+    using Sh = Shape<DH, FP8, CT>;
+    constexpr int NST = Sh::kStages, NK = DH / 16, NB = DH / 32, NT = CT / 8;   // NT: score tiles of 8 keys
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[kW][NST];
     __shared__ float sm_m[kW][kHB], sm_l[kW][kHB];
@@ -141,6 +142,7 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
     }
     __syncwarp();
     const uint32_t stages = tc::smem_u32(ring) + warp * NST * Sh::kStage;
+    const int64_t exps_at = (int64_t)a.c.n_pages * a.c.Hkv * a.c.page * DH;   // FP8: offset of the exponents
     uint32_t it = 0;                 // chunks this warp has asked for, over all segments
     uint32_t used = 0;               // chunks this warp has consumed
     bool ok = true;
@@ -151,11 +153,11 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
         pc.off = 0;
         pc.len = 1;
     } else {
-        pc = piece_of<32 * kW>(a, s, sh);
+        pc = piece_of<32 * kW, CT>(a, s, sh);
     }
     int64_t done = 0;
     while (done < pc.len) {
-        const DecodeKeys dk = decode_keys(a.pos[pc.b], a.window, a.sinks, capacity_of(a), a.c.status);
+        const DecodeKeys<CT> dk = decode_keys<CT>(a.pos[pc.b], a.window, a.sinks, capacity_of(a), a.c.status);
         Segment sg;
         sg.b = pc.b;
         sg.n = dk.n;
@@ -181,7 +183,7 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
 
         int lines = 0;               // lane i: first row of this warp's chunk (asked & ~31) + i in the page arrays
         int asked = 0;               // of this segment
-        auto ask = [&]() {           // whole warp
+        auto ask = [&]() -> uint2 {  // whole warp; returns (FP8) the exponents of K and V row lane % CT
             if ((asked & 31) == 0 && asked + lane < mine) {
                 const int j0 = dk.token(sg.c0 + warp + (asked + lane) * kW), nth = j0 / a.c.page;
                 int id = a.c.table[(int64_t)sg.b * a.c.max_pages + nth];
@@ -196,23 +198,29 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                 const int st = it % NST;
                 const uint32_t dst = stages + st * Sh::kStage;
                 uint64_t *bar = &bars[warp][st];
-                tc::mbar_arrive_expect_tx(bar, Sh::kTx);
+                tc::mbar_arrive_expect_tx(bar, Sh::kStage);
 #pragma unroll
                 for (int c = 0; c < (FP8 ? 1 : DH / 64); ++c) {
-                    tc::tma_load_2d(dst + c * 2048, &tm_k, c * 64, line, bar);
-                    tc::tma_load_2d(dst + Sh::kTile + c * 2048, &tm_v, c * 64, line, bar);
-                }
-                if constexpr (FP8) {
-                    const int64_t all = (int64_t)a.c.n_pages * a.c.Hkv * a.c.page;
-                    const int64_t at = all * DH + (int64_t)line * NB;
-                    tc::bulk_load(dst + 2 * Sh::kTile, (const uint8_t *)a.c.k_pages + at, Sh::kExps, bar);
-                    tc::bulk_load(dst + 2 * Sh::kTile + Sh::kExps, (const uint8_t *)a.c.v_pages + at, Sh::kExps, bar);
+                    tc::tma_load_2d(dst + c * CT * 128, &tm_k, c * 64, line, bar);
+                    tc::tma_load_2d(dst + Sh::kTile + c * CT * 128, &tm_v, c * 64, line, bar);
                 }
             }
             ++it;
             ++asked;
+            if constexpr (FP8) {
+                const int64_t at = exps_at + ((int64_t)line + (lane & (CT - 1))) * NB;
+                const uint8_t *ks = (const uint8_t *)a.c.k_pages + at, *vs = (const uint8_t *)a.c.v_pages + at;
+                if constexpr (NB == 4)
+                    return make_uint2(__ldg(reinterpret_cast<const uint32_t *>(ks)), __ldg(reinterpret_cast<const uint32_t *>(vs)));
+                else   // unused bytes repeat used ones
+                    return make_uint2(__ldg(reinterpret_cast<const uint16_t *>(ks)) * 0x00010001u,
+                                      __ldg(reinterpret_cast<const uint16_t *>(vs)) * 0x00010001u);
+            }
+            return make_uint2(0, 0);
         };
-        for (int i = 0; i < NST && i < mine; ++i) ask();
+        uint2 exps[NST];             // FP8: of the next chunks
+#pragma unroll
+        for (int i = 0; i < NST; ++i) exps[i] = i < mine ? ask() : make_uint2(0, 0);
 
         // Q fragments: 16 heads x 16 channels a step; rows past the group are zero.  FP8: channels 4 cq .. + 3 of the
         // step, as its code words have them
@@ -268,6 +276,8 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                 }
             q16 = __all_sync(0xffffffffu, q16);
         }
+        // weights are held times 2^kUp; with the maximum at most kSlack above the reference they stay below 2^15 (fp16)
+        constexpr float kSlack = FP8 ? 4.f : 8.f, kUp = FP8 ? 11.f : 0.f, kUnUp = FP8 ? 0x1p-11f : 1.f;
         int Ek = 0, Ev = -128;       // reference exponents (Ev: none yet)
         float o[2 * NK][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // heads gr and gr + 8
 #pragma unroll
@@ -281,62 +291,36 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
             if (!ok) break;
             const uint32_t kt = stages + st * Sh::kStage, vt = kt + Sh::kTile;
             const int j0 = dk.token(sg.c0 + warp + i * kW);
-            const bool whole = token_seen(dk, j0, a.sinks) && token_seen(dk, j0 + 15, a.sinks) &&
-                               (j0 >= dk.w0 || j0 + 15 < a.sinks);
+            const bool whole = dk.all_seen(j0, a.sinks);
             if (!whole) {            // V rows that are not seen: zeros
-                for (int r = 0; r < 16; ++r) {
-                    if (token_seen(dk, j0 + r, a.sinks)) continue;
+                for (int r = 0; r < CT; ++r) {
+                    if (dk.seen(j0 + r, a.sinks)) continue;
                     uint8_t *v = ring + (warp * NST + st) * Sh::kStage + Sh::kTile;
-                    if (lane < Sh::kTile / 256)
-                        *reinterpret_cast<uint4 *>(v + tile_offset<DH, FP8>(r, lane)) = make_uint4(0, 0, 0, 0);
+                    if (lane < DH * (FP8 ? 1 : 2) / 16)
+                        *reinterpret_cast<uint4 *>(v + tile_offset<DH, FP8, CT>(r, lane)) = make_uint4(0, 0, 0, 0);
                 }
                 tc::fence_async_smem();   // ordered before the next TMA write of this stage
                 __syncwarp();
             }
-            // FP8: the exponents of the K rows (gr, gr + 8) and V rows (2 cq, + 1, + 8, + 9) this thread touches; dk4, dv4:
-            // e - E + 8 by byte, in 0 .. 15 on the fast paths
-            uint32_t ke[2], ve[4], dk4[2], dv4[4];
+            // FP8: this lane's words of exponents against the references: z = 4 (e - E + 15) by byte, the upper byte of
+            // the fp16 number 2^(e - E), where e - E is in [-8, 7]
+            uint2 ew = exps[0], z = ew;
             bool k_fast = q16, v_fast = true;
             if constexpr (FP8) {
-                const uint8_t *ex = ring + (warp * NST + st) * Sh::kStage + 2 * Sh::kTile;
-                auto word = [&](int r) -> uint32_t {   // unused bytes repeat used ones
-                    if constexpr (NB == 4) return *reinterpret_cast<const uint32_t *>(ex + r * 4);
-                    else return *reinterpret_cast<const uint16_t *>(ex + r * 2) * 0x00010001u;
+                const bool hidden = !whole && !dk.seen(j0 + (lane & (CT - 1)), a.sinks);
+                auto offset = [&](uint32_t e, int E, uint32_t &zz) {
+                    const uint32_t d = hidden ? 0x08080808u : __vsub4(e, (uint32_t)((E - 8) & 255) * 0x01010101u);
+                    zz = (d + 0x07070707u) << 2;
+                    return !__any_sync(0xffffffffu, d & 0xF0F0F0F0u);
                 };
-#pragma unroll
-                for (int t = 0; t < 2; ++t) ke[t] = word(gr + 8 * t);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) ve[t] = word(16 + 2 * cq + (t & 1) + 8 * (t >> 1));
-                uint32_t hide_k = 0, hide_v = 0;   // rows that are not seen
-                if (!whole) {
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        if (!token_seen(dk, j0 + gr + 8 * t, a.sinks)) hide_k |= 1u << t;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        if (!token_seen(dk, j0 + 2 * cq + (t & 1) + 8 * (t >> 1), a.sinks)) hide_v |= 1u << t;
+                auto largest = [&](uint32_t e) { return __reduce_max_sync(0xffffffffu, hidden ? -126 : max4s(e)); };
+                if (!offset(ew.x, Ek, z.x) && k_fast) {
+                    const int top = largest(ew.x);
+                    if (abs(top) < 60) Ek = top;
+                    k_fast = offset(ew.x, Ek, z.x);
                 }
-                auto offsets = [&](const uint32_t *e, uint32_t *d, int n, int E, uint32_t hide) {
-                    uint32_t out = 0;
-                    for (int t = 0; t < n; ++t) {
-                        d[t] = hide >> t & 1 ? 0x08080808u : __vsub4(e[t], (uint32_t)((E - 8) & 255) * 0x01010101u);
-                        out |= d[t];
-                    }
-                    return !__any_sync(0xffffffffu, out & 0xF0F0F0F0u);
-                };
-                auto largest = [&](const uint32_t *e, int n, uint32_t hide) {
-                    int m = -126;
-                    for (int t = 0; t < n; ++t)
-                        if (!(hide >> t & 1)) m = max(m, max4s(e[t]));
-                    return __reduce_max_sync(0xffffffffu, m);
-                };
-                if (k_fast && !offsets(ke, dk4, 2, Ek, hide_k)) {
-                    const int top = largest(ke, 2, hide_k);
-                    k_fast = abs(top) < 60 && offsets(ke, dk4, 2, top, hide_k);
-                    if (k_fast) Ek = top;
-                }
-                if (Ev == -128 || !offsets(ve, dv4, 4, Ev, hide_v)) {
-                    const int top = largest(ve, 4, hide_v);
+                if (Ev == -128 || !offset(ew.y, Ev, z.y)) {
+                    const int top = largest(ew.y);
                     if (top > Ev) {
                         const float f = pow2_or_0(Ev - top);   // no value yet: O is zero
                         Ev = top;
@@ -345,51 +329,63 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
 #pragma unroll
                             for (int e = 0; e < 4; ++e) o[j][e] *= f;
                     }
-                    v_fast = offsets(ve, dv4, 4, Ev, hide_v);
+                    v_fast = offset(ew.y, Ev, z.y);
                 }
             }
-            float sc[2][4], sd[2][4];   // even and odd steps: two shorter chains of products
+            // word of tile t's key gr, and of keys 2 cq + (t & 1) + 8 (t / 2)
+            auto k_word = [&](uint32_t w, int t) { return __shfl_sync(0xffffffffu, w, gr + 8 * t); };
+            auto v_word = [&](uint32_t w, int t) { return __shfl_sync(0xffffffffu, w, 2 * cq + (t & 1) + 8 * (t >> 1)); };
+            float sc[NT][4];
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[t][e] = sd[t][e] = 0.f;
+                for (int e = 0; e < 4; ++e) sc[t][e] = 0.f;
             if constexpr (!FP8) {
 #pragma unroll
-                for (int k = 0; k < NK; ++k) {
-                    uint32_t b[4];
-                    ldsm4(kt + tile_offset<DH, FP8>((lane & 7) + ((lane >> 4) & 1) * 8, 2 * k + ((lane >> 3) & 1)), b);
-                    mma16816(k & 1 ? sd[0] : sc[0], q[k], b[0], b[1]);
-                    mma16816(k & 1 ? sd[1] : sc[1], q[k], b[2], b[3]);
-                }
-            } else {
-                if (k_fast) {
-                    const uint32_t z[2] = {dk4[0] + 0x07070707u, dk4[1] + 0x07070707u};   // fp16 exponent fields
+                for (int k = 0; k < NK; ++k)
 #pragma unroll
-                    for (int k = 0; k < NK / 2; ++k) {   // steps 2 k and 2 k + 1: block k
-                        uint32_t w[4];
-                        ldsm4(kt + tile_offset<DH, FP8>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4)), w);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t b0, b1;
-                            // byte k of z in both halves
-                            const uint32_t f = __byte_perm(z[e & 1], 0, 0x4040 + 0x0101 * k) << 10;
-                            codes_f16(w[e], f, f, b0, b1);
-                            mma16816h(e >> 1 ? sd[e & 1] : sc[e & 1], q[2 * k + (e >> 1)], b0, b1);
-                        }
+                    for (int t = 0; t < NT; t += 2) {
+                        uint32_t b[4];
+                        ldsm4(kt + tile_offset<DH, FP8, CT>(8 * t + (lane & 7) + ((lane >> 4) & 1) * 8, 2 * k + ((lane >> 3) & 1)), b);
+                        mma16816(sc[t], q[k], b[0], b[1]);
+                        mma16816(sc[t + 1], q[k], b[2], b[3]);
                     }
-                } else {
+            } else {
+                uint32_t f[NT];
 #pragma unroll
+                for (int t = 0; t < NT; ++t) f[t] = k_word(k_fast ? z.x : ew.x, t);
+                if (k_fast) {
+#pragma unroll
+                    for (int k = 0; k < NK / 2; ++k)   // steps 2 k and 2 k + 1: block k
+#pragma unroll
+                        for (int t = 0; t < NT; t += 2) {
+                            uint32_t w[4];
+                            ldsm4(kt + tile_offset<DH, FP8, CT>(8 * t + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4)), w);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t b0, b1;
+                                // byte k above a zero byte, twice
+                                const uint32_t fk = __byte_perm(f[t + (e & 1)], 0, 0x0404 + 0x1010 * k);
+                                codes_f16(w[e], fk, fk, b0, b1);
+                                mma16816h(sc[t + (e & 1)], q[2 * k + (e >> 1)], b0, b1);
+                            }
+                        }
+                } else {
                     for (int k = 0; k < NK / 2; ++k) {
-                        uint32_t w[4], qb[2][4];
-                        ldsm4(kt + tile_offset<DH, FP8>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4)), w);
+                        uint32_t qb[2][4];
                         load_q(2 * k, qb[0]);
                         load_q(2 * k + 1, qb[1]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t b0, b1;
-                            const float f = lp::pow2f((int8_t)(ke[e & 1] >> (8 * k)));
-                            codes_bf16(w[e], f, f, f, f, b0, b1);
-                            mma16816(e >> 1 ? sd[e & 1] : sc[e & 1], qb[e >> 1], b0, b1);
+                        for (int t = 0; t < NT; t += 2) {
+                            uint32_t w[4];
+                            ldsm4(kt + tile_offset<DH, FP8, CT>(8 * t + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4)), w);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t b0, b1;
+                                const float fk = lp::pow2f((int8_t)(f[t + (e & 1)] >> (8 * k)));
+                                codes_bf16(w[e], fk, fk, fk, fk, b0, b1);
+                                mma16816(sc[t + (e & 1)], qb[e >> 1], b0, b1);
+                            }
                         }
                     }
                 }
@@ -397,22 +393,25 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
             const bool scaled = FP8 && k_fast;   // undo the scales of Q and K
             const float s0 = scaled ? scale * lp::pow2f(up0 + Ek) : scale, s1 = scaled ? scale * lp::pow2f(up1 + Ek) : scale;
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    sc[t][e] = (sc[t][e] + sd[t][e]) * (e < 2 ? s0 : s1);
-                    if (!whole && !token_seen(dk, j0 + 8 * t + 2 * cq + (e & 1), a.sinks)) sc[t][e] = -INFINITY;
+                    sc[t][e] *= e < 2 ? s0 : s1;
+                    if (!whole && !dk.seen(j0 + 8 * t + 2 * cq + (e & 1), a.sinks)) sc[t][e] = -INFINITY;
                 }
-            float n0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-            float n1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+            float n0 = m0, n1 = m1;
 #pragma unroll
-            for (int x = 1; x < 4; x <<= 1) {
-                n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
-                n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
+            for (int t = 0; t < NT; ++t) {
+                n0 = fmaxf(n0, fmaxf(sc[t][0], sc[t][1]));
+                n1 = fmaxf(n1, fmaxf(sc[t][2], sc[t][3]));
             }
-            n0 = fmaxf(n0, m0);
-            n1 = fmaxf(n1, m1);
-            if (__any_sync(0xffffffffu, n0 != m0 || n1 != m1)) {
+            // m is the reference of the exponentials, at most kSlack (exp2 units) below the maximum
+            if (__any_sync(0xffffffffu, n0 > m0 + kSlack || n1 > m1 + kSlack)) {
+#pragma unroll
+                for (int x = 1; x < 4; x <<= 1) {
+                    n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
+                    n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
+                }
                 // -inf - -inf: a head without a finite score yet has no sum to rescale
                 const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
                 m0 = n0;
@@ -427,10 +426,9 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                     o[j][3] *= f1;
                 }
             }
-            constexpr float kUp = FP8 ? 15.f : 0.f;   // weights times 2^kUp
             const float r0 = m0 == -INFINITY ? 0.f : m0 - kUp, r1 = m1 == -INFINITY ? 0.f : m1 - kUp;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < NT; ++t) {
                 sc[t][0] = ex2(sc[t][0] - r0);
                 sc[t][1] = ex2(sc[t][1] - r0);
                 sc[t][2] = ex2(sc[t][2] - r1);
@@ -438,67 +436,76 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                 l0 += sc[t][0] + sc[t][1];
                 l1 += sc[t][2] + sc[t][3];
             }
-            uint32_t p[4];
-            if (FP8 && v_fast) {
+            uint32_t p[CT / 16][4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) p[t] = pack2h(sc[t >> 1][2 * (t & 1)], sc[t >> 1][2 * (t & 1) + 1]);
-            } else {
+            for (int x = 0; x < CT / 16; ++x)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) p[t] = pack2(sc[t >> 1][2 * (t & 1)], sc[t >> 1][2 * (t & 1) + 1]);
-            }
+                for (int t = 0; t < 4; ++t) {
+                    const float lo = sc[2 * x + (t >> 1)][2 * (t & 1)], hi = sc[2 * x + (t >> 1)][2 * (t & 1) + 1];
+                    p[x][t] = FP8 && v_fast ? pack2h(lo, hi) : pack2(lo, hi);
+                }
             if constexpr (!FP8) {
 #pragma unroll
-                for (int j = 0; j < NK; ++j) {
-                    uint32_t b[4];
-                    ldsm4t(vt + tile_offset<DH, FP8>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * j + (lane >> 4)), b);
-                    mma16816(o[2 * j], p, b[0], b[1]);
-                    mma16816(o[2 * j + 1], p, b[2], b[3]);
-                }
+                for (int x = 0; x < CT / 16; ++x)
+#pragma unroll
+                    for (int j = 0; j < NK; ++j) {
+                        uint32_t b[4];
+                        ldsm4t(vt + tile_offset<DH, FP8, CT>(16 * x + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * j + (lane >> 4)), b);
+                        mma16816(o[2 * j], p[x], b[0], b[1]);
+                        mma16816(o[2 * j + 1], p[x], b[2], b[3]);
+                    }
             } else {
                 // granules 2 j and 2 j + 1 of the row: block j.  A word of ldmatrix.trans: two channels of key 2 cq, then the
-                // same of key 2 cq + 1 (t: keys 0..7, 8..15)
-                if (v_fast) {
+                // same of key 2 cq + 1 (t: keys 0..7, 8..15 of the 16)
 #pragma unroll
-                    for (int j = 0; j < NK / 2; ++j) {
-                        uint32_t w[4], f[2];
-                        ldsm4t(vt + tile_offset<DH, FP8>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * j + (lane >> 4)), w);
+                for (int x = 0; x < CT / 16; ++x) {
+                    uint32_t fv[4];
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)
-                            f[t] = ((__byte_perm(dv4[2 * t], dv4[2 * t + 1], 0x0400 + 0x0101 * j) & 0x000F000Fu) +
-                                    0x00070007u) << 10;
+                    for (int t = 0; t < 4; ++t) fv[t] = v_word(v_fast ? z.y : ew.y, 4 * x + t);
+                    if (v_fast) {
 #pragma unroll
-                        for (int gi = 0; gi < 2; ++gi) {
-                            uint32_t c0[2], c1[2];
+                        for (int j = 0; j < NK / 2; ++j) {
+                            uint32_t w[4], f[2];
+                            ldsm4t(vt + tile_offset<DH, FP8, CT>(16 * x + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * j + (lane >> 4)), w);
 #pragma unroll
                             for (int t = 0; t < 2; ++t)
-                                codes_f16(__byte_perm(w[2 * gi + t], 0, 0x3120), f[t], f[t], c0[t], c1[t]);
-                            mma16816h(o[2 * (2 * j + gi)], p, c0[0], c0[1]);
-                            mma16816h(o[2 * (2 * j + gi) + 1], p, c1[0], c1[1]);
-                        }
-                    }
-                } else {
+                                f[t] = __byte_perm(fv[2 * t], fv[2 * t + 1], 0x4000 + 0x1010 * j) & 0xFF00FF00u;
 #pragma unroll
-                    for (int j = 0; j < NK / 2; ++j) {
-                        uint32_t w[4];
-                        ldsm4t(vt + tile_offset<DH, FP8>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * j + (lane >> 4)), w);
+                            for (int gi = 0; gi < 2; ++gi) {
+                                uint32_t c0[2], c1[2];
 #pragma unroll
-                        for (int gi = 0; gi < 2; ++gi) {
-                            uint32_t c0[2], c1[2];
-#pragma unroll
-                            for (int t = 0; t < 2; ++t) {
-                                // a row that is not seen has codes 0; its exponent may be anything
-                                const float fa = pow2_or_0(min((int8_t)(ve[2 * t] >> (8 * j)) - Ev, 127));
-                                const float fb = pow2_or_0(min((int8_t)(ve[2 * t + 1] >> (8 * j)) - Ev, 127));
-                                codes_bf16(__byte_perm(w[2 * gi + t], 0, 0x3120), fa, fb, fa, fb, c0[t], c1[t]);
+                                for (int t = 0; t < 2; ++t)
+                                    codes_f16(__byte_perm(w[2 * gi + t], 0, 0x3120), f[t], f[t], c0[t], c1[t]);
+                                mma16816h(o[2 * (2 * j + gi)], p[x], c0[0], c0[1]);
+                                mma16816h(o[2 * (2 * j + gi) + 1], p[x], c1[0], c1[1]);
                             }
-                            mma16816(o[2 * (2 * j + gi)], p, c0[0], c0[1]);
-                            mma16816(o[2 * (2 * j + gi) + 1], p, c1[0], c1[1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < NK / 2; ++j) {
+                            uint32_t w[4];
+                            ldsm4t(vt + tile_offset<DH, FP8, CT>(16 * x + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * j + (lane >> 4)), w);
+#pragma unroll
+                            for (int gi = 0; gi < 2; ++gi) {
+                                uint32_t c0[2], c1[2];
+#pragma unroll
+                                for (int t = 0; t < 2; ++t) {
+                                    // a row that is not seen has codes 0; its exponent may be anything
+                                    const float fa = pow2_or_0(min((int8_t)(fv[2 * t] >> (8 * j)) - Ev, 127));
+                                    const float fb = pow2_or_0(min((int8_t)(fv[2 * t + 1] >> (8 * j)) - Ev, 127));
+                                    codes_bf16(__byte_perm(w[2 * gi + t], 0, 0x3120), fa, fb, fa, fb, c0[t], c1[t]);
+                                }
+                                mma16816(o[2 * (2 * j + gi)], p[x], c0[0], c0[1]);
+                                mma16816(o[2 * (2 * j + gi) + 1], p[x], c1[0], c1[1]);
+                            }
                         }
                     }
                 }
             }
             __syncwarp();            // every lane has read the stage
-            if (asked < mine) ask();
+#pragma unroll
+            for (int x = 0; x + 1 < NST; ++x) exps[x] = exps[x + 1];
+            exps[NST - 1] = asked < mine ? ask() : make_uint2(0, 0);
         }
 
         // ------------------------------------------------ join of the warps
@@ -508,12 +515,12 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
         if constexpr (FP8) {         // undo the weights' and V's references
             const float f = pow2_or_0(Ev);
-            l0 *= 0x1p-15f;
-            l1 *= 0x1p-15f;
+            l0 *= kUnUp;
+            l1 *= kUnUp;
 #pragma unroll
             for (int j = 0; j < 2 * NK; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[j][e] = o[j][e] * 0x1p-15f * f;
+                for (int e = 0; e < 4; ++e) o[j][e] = o[j][e] * kUnUp * f;
         }
         if (cq == 0) {
             sm_m[warp][gr] = m0;
@@ -584,23 +591,23 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
         tc::mbar_wait(&bars[warp][used % NST], (used / NST) & 1, a.c.status);
 }
 
-template <int DH, bool FP8>
+template <int DH, bool FP8, int CT>
 hcsa_status launch(const DecodeArgs &a, cudaStream_t st) {
-    using Sh = Shape<DH, FP8>;
-    auto kernel = swa_decode_tc_kernel<DH, FP8>;
+    using Sh = Shape<DH, FP8, CT>;
+    auto kernel = swa_decode_tc_kernel<DH, FP8, CT>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) != cudaSuccess)
         return HCSA_ERR_CUDA;
     CUtensorMap mk, mv;
     const uint64_t rows = (uint64_t)a.c.n_pages * a.c.Hkv * a.c.page;
-    const bool made = FP8 ? make_tmap_u8_2d(&mk, a.c.k_pages, DH, rows, DH, DH, 16) &&
-                                make_tmap_u8_2d(&mv, a.c.v_pages, DH, rows, DH, DH, 16)
-                          : make_tmap_bf16_2d(&mk, a.c.k_pages, DH, rows, DH * 2, 64, 16, true) &&
-                                make_tmap_bf16_2d(&mv, a.c.v_pages, DH, rows, DH * 2, 64, 16, true);
+    const bool made = FP8 ? make_tmap_u8_2d(&mk, a.c.k_pages, DH, rows, DH, DH, CT) &&
+                                make_tmap_u8_2d(&mv, a.c.v_pages, DH, rows, DH, DH, CT)
+                          : make_tmap_bf16_2d(&mk, a.c.k_pages, DH, rows, DH * 2, 64, CT, true) &&
+                                make_tmap_bf16_2d(&mv, a.c.v_pages, DH, rows, DH * 2, 64, CT, true);
     if (!made) return HCSA_ERR_CUDA;
     const int G = a.H / a.c.Hkv, units = a.c.Hkv * ((G + kHB - 1) / kHB);
     const bool direct = decode_direct(a);
     if (direct && (int64_t)a.c.B * units > INT32_MAX) return HCSA_ERR_UNSUPPORTED;
-    const int grid = direct ? a.c.B * units : decode_grid();
+    const int grid = direct ? a.c.B * units : decode_grid(kPerSM);
     Split s = make_split(a, units, kHB, grid);
     s.direct = direct;
     kernel<<<grid, 32 * kW, Sh::kSmem, st>>>(a, s, mk, mv);
@@ -612,13 +619,15 @@ hcsa_status launch(const DecodeArgs &a, cudaStream_t st) {
 }  // namespace
 
 int decode_tc_heads() { return kHB; }
+int decode_tc_grid() { return decode_grid(kPerSM); }
 
 // bf16 queries, dh 64 or 128 (any window, sinks, page and group)
 bool decode_tc_supported(int dtype, int dh) { return dtype == HCSA_BF16 && (dh == 64 || dh == 128); }
 
 hcsa_status launch_decode_tc(const DecodeArgs &a, cudaStream_t st) {
-    if (a.c.dh == 64) return a.c.lowprec ? launch<64, true>(a, st) : launch<64, false>(a, st);
-    return a.c.lowprec ? launch<128, true>(a, st) : launch<128, false>(a, st);
+    if (!a.c.lowprec) return a.c.dh == 64 ? launch<64, false, 16>(a, st) : launch<128, false, 16>(a, st);
+    if (a.c.page % 32 == 0) return a.c.dh == 64 ? launch<64, true, 32>(a, st) : launch<128, true, 32>(a, st);
+    return a.c.dh == 64 ? launch<64, true, 16>(a, st) : launch<128, true, 16>(a, st);
 }
 
 }  // namespace hcsa
