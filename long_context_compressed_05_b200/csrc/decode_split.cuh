@@ -101,7 +101,6 @@ __device__ __forceinline__ Piece piece_of(const DecodeArgs &a, const Split &s, i
 
 size_t decode_split_bytes(int B, int grid, int heads, int dh);
 Split make_split(const DecodeArgs &a, int units_per_seq, int heads, int grid);
-int decode_grid(int per_sm);        // CTAs of a split step
 // zero rows of empty slots and join the partials; heads: query heads per unit, blocks: head blocks per key head
 hcsa_status launch_decode_join(const DecodeArgs &a, const Split &s, int heads, int grid, cudaStream_t st);
 bool decode_direct(const DecodeArgs &a);

@@ -39,6 +39,9 @@ struct SwaArgs {
 };
 hcsa_status launch_swa(const SwaArgs &a, cudaStream_t st);        // chooses the kernel
 hcsa_status launch_swa_simt(const SwaArgs &a, cudaStream_t st);
+bool swa_tc_supported(const SwaArgs &a);                          // bf16, dh 64 or 128, a positive scale
+hcsa_status launch_swa_tc(const SwaArgs &a, cudaStream_t st);
+int sm_grid(int per_sm);                                      // SMs of the device x per_sm
 
 // Keys of a block of consecutive queries [t_first, t_last]: `pad` columns for the first tokens that lie
 // outside the window of the block's first query (n_sink of them real), then one column per token from w0

@@ -325,7 +325,7 @@ hcsa_status launch_simt(const DecodeArgs &a, cudaStream_t st) {
     const int G = a.H / a.c.Hkv, units = a.c.Hkv * ((G + HB - 1) / HB);
     const bool direct = decode_direct(a);
     if (direct && (int64_t)a.c.B * units > INT32_MAX) return HCSA_ERR_UNSUPPORTED;
-    const int grid = direct ? a.c.B * units : decode_grid(kPerSM);
+    const int grid = direct ? a.c.B * units : sm_grid(kPerSM);
     Split s = make_split(a, units, HB, grid);
     s.direct = direct;
     swa_decode_simt_kernel<S, FP8, DH><<<grid, 32 * kWarps, smem, st>>>(a, s);
@@ -348,7 +348,7 @@ size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 int decode_simt_heads(int dh) { return dh <= 256 ? 8 : 2; }
 
-int decode_grid(int per_sm) {
+int sm_grid(int per_sm) {
     static int n[64] = {};
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
@@ -408,7 +408,7 @@ hcsa_status launch_decode_simt(const DecodeArgs &a, cudaStream_t st) {
 
 size_t swa_decode_ws_bytes(int dtype, int B, int dh) {
     return decode_tc_supported(dtype, dh) ? decode_split_bytes(B, decode_tc_grid(), decode_tc_heads(), dh)
-                                          : decode_split_bytes(B, decode_grid(kPerSM), decode_simt_heads(dh), dh);
+                                          : decode_split_bytes(B, sm_grid(kPerSM), decode_simt_heads(dh), dh);
 }
 
 hcsa_status launch_swa_decode(const DecodeArgs &a, cudaStream_t st) {

@@ -607,7 +607,7 @@ hcsa_status launch(const DecodeArgs &a, cudaStream_t st) {
     const int G = a.H / a.c.Hkv, units = a.c.Hkv * ((G + kHB - 1) / kHB);
     const bool direct = decode_direct(a);
     if (direct && (int64_t)a.c.B * units > INT32_MAX) return HCSA_ERR_UNSUPPORTED;
-    const int grid = direct ? a.c.B * units : decode_grid(kPerSM);
+    const int grid = direct ? a.c.B * units : sm_grid(kPerSM);
     Split s = make_split(a, units, kHB, grid);
     s.direct = direct;
     kernel<<<grid, 32 * kW, Sh::kSmem, st>>>(a, s, mk, mv);
@@ -619,7 +619,7 @@ hcsa_status launch(const DecodeArgs &a, cudaStream_t st) {
 }  // namespace
 
 int decode_tc_heads() { return kHB; }
-int decode_tc_grid() { return decode_grid(kPerSM); }
+int decode_tc_grid() { return sm_grid(kPerSM); }
 
 // bf16 queries, dh 64 or 128 (any window, sinks, page and group)
 bool decode_tc_supported(int dtype, int dh) { return dtype == HCSA_BF16 && (dh == 64 || dh == 128); }

@@ -208,6 +208,8 @@ hcsa_status launch_swa_simt(const SwaArgs &a, cudaStream_t st) {
     return a.dtype == HCSA_F32 ? launch_dh<float>(a, st) : launch_dh<__nv_bfloat16>(a, st);
 }
 
-hcsa_status launch_swa(const SwaArgs &a, cudaStream_t st) { return launch_swa_simt(a, st); }
+hcsa_status launch_swa(const SwaArgs &a, cudaStream_t st) {
+    return swa_tc_supported(a) ? launch_swa_tc(a, st) : launch_swa_simt(a, st);
+}
 
 }  // namespace hcsa
