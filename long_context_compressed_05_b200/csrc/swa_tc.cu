@@ -36,7 +36,7 @@ constexpr float kSlack = 8.f;        // exp2 units
 struct Args {
     SwaArgs a;
     int G, tb;                       // heads per key head, tokens per sub-tile
-    int64_t n_units;
+    uint32_t blocks, n_units;        // blocks of tokens, x key heads
     float scale_log2;
 };
 
@@ -50,7 +50,7 @@ template <int DH> struct Sizes {
 
 template <int NST> struct Bars {
     uint64_t k_full[NST], k_empty[NST], v_full[NST], v_empty[NST];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], drain;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2], drain;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -71,46 +71,69 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint64_t bdesc, 
                  : "memory");
 }
 
-// A block and its key columns, the same in every role.
-struct Unit {
-    int g, t0, t_end;                // key head, first token, end of the block's tokens
-    int w0, pad, sk;                 // window part from token w0 at column pad; columns below sk are first tokens
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Key columns of a block, the same in every role.
+struct Cols {
+    int pad, sk;                     // the window part starts at column pad; columns below sk are first tokens
     int n_tiles;
-    __device__ __forceinline__ int first(int s, int tb) const { return t0 + s * tb; }
-    __device__ __forceinline__ bool exists(int s, int tb) const { return first(s, tb) < t_end; }
-    __device__ __forceinline__ int last(int s, int tb) const { return min(first(s, tb) + tb, t_end) - 1; }
-    // columns of the window of token t
-    __device__ __forceinline__ int hi(int t) const { return t - w0 + pad; }
-    __device__ __forceinline__ int lo(int t, int window) const { return t - window + 1 - w0 + pad; }
+    int hi0, hi1, lo0, lo1;          // of each sub-tile: its last column (-1: no tokens), its first window column
+    __device__ __forceinline__ int hi(int s) const { return s ? hi1 : hi0; }
     // does sub-tile s see a column of tile i?
-    __device__ __forceinline__ bool active(int s, int i, int tb, int window) const {
+    __device__ __forceinline__ bool active(int s, int i) const {
         const int c0 = i * kKT;
-        return exists(s, tb) && c0 <= hi(last(s, tb)) && (c0 < sk || c0 + kKT - 1 >= lo(first(s, tb), window));
+        return c0 <= hi(s) && (c0 < sk || c0 + kKT - 1 >= (s ? lo1 : lo0));
     }
 };
+struct Unit {
+    int g, t0, t_end, w0;            // key head, tokens, first token of the window part
+    Cols c;
+    __device__ __forceinline__ int first(int s, int tb) const { return t0 + s * tb; }
+    __device__ __forceinline__ int last(int s, int tb) const { return min(t0 + (s + 1) * tb, t_end) - 1; }
+    // window columns of token t
+    __device__ __forceinline__ int hi(int t) const { return t - w0 + c.pad; }
+    __device__ __forceinline__ int lo(int t, int window) const { return t - window + 1 - w0 + c.pad; }
+};
 
-__device__ __forceinline__ Unit unit_of(const Args &p, int64_t u) {
+__device__ __forceinline__ Unit unit_of(const Args &p, uint32_t u) {
     const SwaArgs &a = p.a;
     Unit x;
-    const int64_t blocks = p.n_units / a.Hkv;
-    x.g = (int)(u % a.Hkv);
-    x.t0 = a.row0 + (int)(blocks - 1 - u / a.Hkv) * 2 * p.tb;   // longest first
+    const uint32_t block = u / (uint32_t)a.Hkv;
+    x.g = (int)(u - block * a.Hkv);
+    x.t0 = a.row0 + (int)(p.blocks - 1 - block) * 2 * p.tb;   // longest first
     x.t_end = min(x.t0 + 2 * p.tb, a.row1);
     const BlockKeys b = block_keys(x.t0, x.t_end - 1, a.window, a.sinks, kGran);
-    x.w0 = b.w0;
-    x.pad = b.pad;
-    x.sk = b.n_sink;
-    if (b.pad >= b.w0) {             // the first tokens reach the window: one run of columns from token 0
-        x.w0 = x.pad = 0;
-        x.sk = a.sinks;
-    }
-    x.n_tiles = (x.hi(x.t_end - 1) + kKT) / kKT;
+    // the first tokens may reach the window: one run of columns from token 0
+    const bool run = b.pad >= b.w0;
+    x.w0 = run ? 0 : b.w0;
+    x.c.pad = run ? 0 : b.pad;
+    x.c.sk = run ? a.sinks : b.n_sink;
+    x.c.n_tiles = (x.hi(x.t_end - 1) + kKT) / kKT;
+    x.c.hi0 = x.hi(x.last(0, p.tb));
+    x.c.hi1 = x.first(1, p.tb) < x.t_end ? x.hi(x.last(1, p.tb)) : -1;
+    x.c.lo0 = x.lo(x.t0, a.window);
+    x.c.lo1 = x.lo(x.first(1, p.tb), a.window);
     return x;
 }
 // k-th block of this CTA, or -1
-__device__ __forceinline__ int64_t nth_unit(const Args &p, int64_t k) {
-    const int64_t u = k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    return u < p.n_units ? u : -1;
+__device__ __forceinline__ int nth_unit(const Args &p, int k) {
+    const uint32_t u = (uint32_t)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    return u < p.n_units ? (int)u : -1;
 }
 
 template <int DH>
@@ -141,6 +164,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             tc::mbar_init(&bars->q_full[s], 1);
             tc::mbar_init(&bars->q_empty[s], 1);
             tc::mbar_init(&bars->s_full[s], 1);
+            tc::mbar_init(&bars->p_half[s], 4);
             tc::mbar_init(&bars->p_full[s], 4);
             tc::mbar_init(&bars->o_full[s], 1);
             tc::mbar_init(&bars->o_empty[s], 4);
@@ -162,7 +186,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (lane == 0) {
             uint32_t it = 0, nq[2] = {0, 0}, nk = 0, nv = 0;   // tiles; loads issued
             auto load_q = [&](const Unit &x, int s) {
-                if (!x.exists(s, p.tb)) return;
+                if (x.c.hi(s) < 0) return;
                 if (nq[s]) ok = ok && tc::mbar_wait(&bars->q_empty[s], (nq[s] - 1) & 1, a.status);
                 if (!ok) return;
                 tc::mbar_arrive_expect_tx(&bars->q_full[s], NC * 128 * p.tb * p.G);
@@ -181,22 +205,22 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 tc::mbar_arrive_expect_tx(&full[st], Sz::kTile);
                 for (int c = 0; c < NC; ++c) {
                     const int x0 = x.g * DH + c * 64;
-                    if (c0 >= x.pad) {
-                        tc::tma_load_2d(dst + c * Sz::kChunk, v ? &tm_v : &tm_k, x0, x.w0 + c0 - x.pad, &full[st]);
+                    if (c0 >= x.c.pad) {
+                        tc::tma_load_2d(dst + c * Sz::kChunk, v ? &tm_v : &tm_k, x0, x.w0 + c0 - x.c.pad, &full[st]);
                     } else {
                         for (int r = 0; r < kKT; r += kGran)
                             tc::tma_load_2d(dst + c * Sz::kChunk + r * 128, v ? &tm_v16 : &tm_k16, x0,
-                                            c0 + r < x.pad ? c0 + r : x.w0 + c0 + r - x.pad, &full[st]);
+                                            c0 + r < x.c.pad ? c0 + r : x.w0 + c0 + r - x.c.pad, &full[st]);
                     }
                 }
                 ++(v ? nv : nk);
             };
-            for (int64_t k = 0; ok; ++k) {
-                const int64_t u = nth_unit(p, k);
+            for (int k = 0; ok; ++k) {
+                const int u = nth_unit(p, k);
                 if (u < 0) break;
                 const Unit x = unit_of(p, u);
                 load_q(x, 0);
-                for (int i = 0; i < x.n_tiles && ok; ++i, ++it) {
+                for (int i = 0; i < x.c.n_tiles && ok; ++i, ++it) {
                     load_kv(x, i, false);
                     if (i == 0) load_q(x, 1);
                     if (ok) load_kv(x, i, true);
@@ -217,34 +241,36 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (lane == 0) {
             uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};   // Q tiles, P tiles, blocks seen
             bool fresh[2] = {true, true};                             // no P V of the block yet
-            struct Cursor { int64_t k; Unit x; int i; uint32_t it; bool valid; };
-            auto start = [&](int64_t k, uint32_t it) {
+            struct Cursor { int k, i; uint32_t it; bool valid; Cols c; };
+            auto start = [&](int k, uint32_t it) {
                 Cursor c;
-                const int64_t u = nth_unit(p, k);
+                const int u = nth_unit(p, k);
                 c.valid = u >= 0;
-                if (c.valid) c.x = unit_of(p, u);
+                if (c.valid) c.c = unit_of(p, u).c;
                 c.k = k;
                 c.i = 0;
                 c.it = it;
                 return c;
             };
-            auto later = [&](const Cursor &c, int s) {   // has the block a further tile for s?  Its last one is always active
-                return c.i < c.x.hi(c.x.last(s, p.tb)) / kKT;
-            };
-            auto active = [&](const Cursor &c, int s) { return c.x.active(s, c.i, p.tb, a.window); };
+            // has the block a further tile for s?  Its last one is always active
+            auto later = [&](const Cursor &c, int s) { return c.i < c.c.hi(s) / kKT; };
+            auto active = [&](const Cursor &c, int s) { return c.c.active(s, c.i); };
             bool in[2] = {false, false};   // an S of the block has been issued
+            const uint64_t q0 = tc::sdesc_sw128(Qs, 16, 1024), k0 = tc::sdesc_sw128(Ks, 16, 1024),
+                           v0 = tc::sdesc_sw128(Vs, Sz::kChunk, 1024);
             auto issue_s = [&](const Cursor &c, int s) {
                 const int st = c.it % NST;
                 if (!in[s]) ok = ok && tc::mbar_wait(&bars->q_full[s], nq[s] & 1, a.status);
                 ok = ok && tc::mbar_wait(&bars->k_full[st], (c.it / NST) & 1, a.status);
                 if (!ok) return;
                 tc::tc_fence_after();
-                const uint32_t qb = Qs + s * Sz::kTile, kb = Ks + st * Sz::kTile;
+                const uint64_t qd = q0 + s * (Sz::kTile >> 4), kd = k0 + st * (Sz::kTile >> 4);
 #pragma unroll
-                for (int k = 0; k < DH / 16; ++k)
-                    tc::mma_bf16(tmem + s * 128, tc::sdesc_sw128(qb + (k >> 2) * Sz::kChunk + 32 * (k & 3), 16, 1024),
-                                 tc::sdesc_sw128(kb + (k >> 2) * Sz::kChunk + 32 * (k & 3), 16, 1024), kIdescS,
+                for (int k = 0; k < DH / 16; ++k) {
+                    constexpr int kC = Sz::kChunk >> 4;
+                    tc::mma_bf16(tmem + s * 128, qd + (k >> 2) * kC + 2 * (k & 3), kd + (k >> 2) * kC + 2 * (k & 3), kIdescS,
                                  k != 0 ? 1u : 0u);
+                }
                 tc::mma_commit(&bars->s_full[s]);
                 in[s] = later(c, s);
                 if (!in[s]) {        // the block's last S of this sub-tile
@@ -254,17 +280,19 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             };
             auto issue_pv = [&](const Cursor &c, int s) {
                 const int st = c.it % NST;
-                ok = ok && tc::mbar_wait(&bars->p_full[s], np[s] & 1, a.status);
                 ok = ok && tc::mbar_wait(&bars->v_full[st], (c.it / NST) & 1, a.status);
                 if (fresh[s] && no[s]) ok = ok && tc::mbar_wait(&bars->o_empty[s], (no[s] - 1) & 1, a.status);
-                if (!ok) return;
-                ++np[s];
-                tc::tc_fence_after();
-                const uint32_t vb = Vs + st * Sz::kTile;
+                const uint64_t vd = v0 + st * (Sz::kTile >> 4);
 #pragma unroll
-                for (int k = 0; k < kKT / 16; ++k)
-                    mma_ts(tmem + kColO + s * 128, tmem + s * 128 + 8 * k, tc::sdesc_sw128(vb + 2048 * k, Sz::kChunk, 1024),
-                           kIdescPV, !fresh[s] || k != 0 ? 1u : 0u);
+                for (int k = 0; k < kKT / 16; ++k) {
+                    if (k == 0) ok = ok && tc::mbar_wait(&bars->p_half[s], np[s] & 1, a.status);
+                    if (k == kKT / 32) ok = ok && tc::mbar_wait(&bars->p_full[s], np[s] & 1, a.status);
+                    if (!ok) return;
+                    if (k % (kKT / 32) == 0) tc::tc_fence_after();
+                    mma_ts(tmem + kColO + s * 128, tmem + s * 128 + 8 * k, vd + 128 * k, kIdescPV,
+                           !fresh[s] || k != 0 ? 1u : 0u);
+                }
+                ++np[s];
                 fresh[s] = !later(c, s);
                 if (fresh[s]) {
                     tc::mma_commit(&bars->o_full[s]);
@@ -273,6 +301,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             };
             Cursor cur = start(0, 0);
             if (cur.valid) {
+#pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (active(cur, s)) issue_s(cur, s);
                 if (ok) tc::mma_commit(&bars->k_empty[cur.it % NST]);
@@ -280,8 +309,9 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             while (cur.valid && ok) {
                 Cursor nxt = cur;
                 ++nxt.it;
-                if (++nxt.i == cur.x.n_tiles) nxt = start(cur.k + 1, cur.it + 1);
-                for (int s = 0; s < 2 && ok; ++s) {
+                if (++nxt.i == cur.c.n_tiles) nxt = start(cur.k + 1, cur.it + 1);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
                     if (active(cur, s)) issue_pv(cur, s);
                     if (ok && nxt.valid && active(nxt, s)) issue_s(nxt, s);
                 }
@@ -309,18 +339,18 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const int tl = r / p.G, hh = r - tl * p.G;
         uint8_t *stage = staging + (warp - 4) * 4096;
         uint32_t ns = 0, nu = 0;     // S tiles and blocks seen
-        for (int64_t kk = 0; ok; ++kk) {
-            const int64_t u = nth_unit(p, kk);
+        for (int kk = 0; ok; ++kk) {
+            const int u = nth_unit(p, kk);
             if (u < 0) break;
             const Unit x = unit_of(p, u);
-            if (!x.exists(s, p.tb)) continue;
+            if (x.c.hi(s) < 0) continue;
             const int ta = x.first(s, p.tb), te = x.last(s, p.tb), t = ta + tl;
             const bool row_ok = tl < p.tb && t <= te;
             const int hi = row_ok ? x.hi(t) : -1, lo = row_ok ? x.lo(t, a.window) : 0;
             float m = -INFINITY, l = 0.f;
             bool first = true;
-            for (int i = 0; i < x.n_tiles; ++i) {
-                if (!x.active(s, i, p.tb, a.window)) continue;
+            for (int i = 0; i < x.c.n_tiles; ++i) {
+                if (!x.c.active(s, i)) continue;
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->s_full[s], ns & 1, a.status));
                 if (!ok) break;
                 ++ns;
@@ -330,22 +360,28 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 for (int c = 0; c < kKT; c += 32) tc::tmem_ld32(tS + c, v + c);
                 tc::tmem_ld_wait();
                 const int c0 = i * kKT;
-                const bool clean = c0 + kKT - 1 <= x.hi(ta) && (c0 >= x.lo(te, a.window) || c0 + kKT <= x.sk);
+                const bool clean = c0 + kKT - 1 <= x.hi(ta) && (c0 >= x.lo(te, a.window) || c0 + kKT <= x.c.sk);
                 if (!clean) {
 #pragma unroll
                     for (int q = 0; q < kKT; q += 32) {
                         // bit c: column c0 + q + c is seen
                         auto upto = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
                         const int cg = c0 + q;
-                        const uint32_t bits = upto(hi + 1 - cg) & (~upto(lo - cg) | upto(x.sk - cg));
+                        const uint32_t bits = upto(hi + 1 - cg) & (~upto(lo - cg) | upto(x.c.sk - cg));
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
                             if (!(bits >> c & 1)) v[q + c] = -INFINITY;
                     }
                 }
-                float mt = v[0];
+                float mx[8];
 #pragma unroll
-                for (int c = 1; c < kKT; ++c) mt = fmaxf(mt, v[c]);
+                for (int c = 0; c < 8; ++c) mx[c] = fmaxf(v[c], v[c + 8]);
+#pragma unroll
+                for (int c = 16; c < kKT; c += 16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mx[e] = fmaxf(mx[e], fmaxf(v[c + e], v[c + e + 8]));
+                float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                 fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
                 mt *= p.scale_log2;
                 const bool need = mt > m + kSlack;
                 if (__any_sync(0xffffffffu, need)) {
@@ -367,25 +403,29 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 }
                 first = false;
                 const float ref = m == -INFINITY ? 0.f : m;   // a row that has seen no key yet: every weight 0
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), ref2 = f2(-ref, -ref);
+                uint64_t sum[4] = {0, 0, 0, 0};   // pairs of zeros
 #pragma unroll
                 for (int q = 0; q < kKT; q += 64) {
                     float w[32];
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        const float e0 = ex2(fmaf(v[q + 2 * c], p.scale_log2, -ref));
-                        const float e1 = ex2(fmaf(v[q + 2 * c + 1], p.scale_log2, -ref));
-                        sum[c & 1] += e0;
-                        sum[2 + (c & 1)] += e1;
+                        float e0, e1;
+                        unf2(fma2(f2(v[q + 2 * c], v[q + 2 * c + 1]), sc2, ref2), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        sum[c & 3] = add2(sum[c & 3], f2(e0, e1));
                         w[c] = __uint_as_float(pack2(e0, e1));
                     }
                     tc::tmem_st32(tS + q / 2, w);
+                    tc::tmem_st_wait();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(q == 0 ? &bars->p_half[s] : &bars->p_full[s]);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tc::tmem_st_wait();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars->p_full[s]);
+                float s0, s1;
+                unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+                l += s0 + s1;
             }
             if (!ok) break;
             // ------------------------------------------------ output
@@ -431,10 +471,10 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             // rows that are not finite: by a value that they do not see? (the columns loaded for the block)
             for (unsigned bad = __ballot_sync(0xffffffffu, row_ok && zero != 0.f); bad; bad &= bad - 1) {
                 const int row = quad * 32 + __ffs(bad) - 1, rt = ta + row / p.G;
-                const int end = min(a.row1, x.w0 + x.n_tiles * kKT - x.pad);
+                const int end = min(a.row1, x.w0 + x.c.n_tiles * kKT - x.c.pad);
                 if (values_bad<__nv_bfloat16>(a, x.g, x.w0, (int64_t)rt - a.window + 1, lane) ||
                     values_bad<__nv_bfloat16>(a, x.g, rt + 1, end, lane) ||
-                    (x.pad && values_bad<__nv_bfloat16>(a, x.g, x.sk, x.pad, lane)))
+                    (x.c.pad && values_bad<__nv_bfloat16>(a, x.g, x.c.sk, x.c.pad, lane)))
                     attend_row<__nv_bfloat16>(a, rt, x.g * p.G + row % p.G, lane);
             }
         }
@@ -454,7 +494,9 @@ hcsa_status launch(const SwaArgs &a, cudaStream_t st) {
     p.a = a;
     p.G = a.H / a.Hkv;
     p.tb = kRows / p.G;
-    p.n_units = (((int64_t)a.row1 - a.row0 + 2 * p.tb - 1) / (2 * p.tb)) * a.Hkv;
+    p.blocks = (uint32_t)((a.row1 - a.row0 + 2 * p.tb - 1) / (2 * p.tb));
+    if ((int64_t)p.blocks * a.Hkv > INT32_MAX / 2) return HCSA_ERR_UNSUPPORTED;
+    p.n_units = p.blocks * a.Hkv;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     CUtensorMap q, k, v, k16, v16;
     const uint64_t rows = a.row1, nkv = (uint64_t)a.Hkv * DH;   // tokens behind the row range are not read
@@ -464,8 +506,7 @@ hcsa_status launch(const SwaArgs &a, cudaStream_t st) {
         !make_tmap_bf16_2d(&k16, a.k, nkv, rows, a.ld_k * 2, 64, kGran, true) ||
         !make_tmap_bf16_2d(&v16, a.v, nkv, rows, a.ld_v * 2, 64, kGran, true))
         return HCSA_ERR_CUDA;
-    const int sms = sm_grid(1);
-    const unsigned grid = (unsigned)(p.n_units < sms ? p.n_units : sms);
+    const unsigned sms = sm_grid(1), grid = p.n_units < sms ? p.n_units : sms;
     swa_tc_kernel<DH><<<grid, kThreads, Sz::kSmem, st>>>(q, k, v, k16, v16, p);
     count_launch();
     return check_launch();
