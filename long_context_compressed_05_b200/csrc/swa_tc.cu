@@ -63,11 +63,26 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// The issuing warp runs its loop with all lanes, so that addresses and descriptors stay in uniform registers; one
+// elected lane (always the same) issues.  With a single active lane each product cost 120 cycles to issue.
+// D[tmem] (+)= A[smem] B[smem]^T
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc),
+                 "r"(accumulate)
+                 : "memory");
+}
 // D[tmem] (+)= A[tmem] B[smem]: A's row i in lane i, two bf16 per 32-bit column
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(at), "l"(bdesc), "r"(idesc),
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(at), "l"(bdesc), "r"(idesc),
                  "r"(accumulate)
+                 : "memory");
+}
+// mma_commit by the elected lane
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar))
                  : "memory");
 }
 
@@ -152,7 +167,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(tmem_slot + 4) + 1023) & ~uintptr_t(1023));
     uint8_t *staging = base + (2 + 2 * NST) * Sz::kTile;
     const uint32_t Qs = tc::smem_u32(base), Ks = Qs + 2 * Sz::kTile, Vs = Ks + NST * Sz::kTile;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
             tc::mbar_init(&bars->k_full[i], 1);
@@ -176,7 +191,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // uniform
     bool ok = true;
 
     if (warp < 4) {
@@ -238,7 +253,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer
-        if (lane == 0) {
+        {
             uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};   // Q tiles, P tiles, blocks seen
             bool fresh[2] = {true, true};                             // no P V of the block yet
             struct Cursor { int k, i; uint32_t it; bool valid; Cols c; };
@@ -268,13 +283,13 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
                 for (int k = 0; k < DH / 16; ++k) {
                     constexpr int kC = Sz::kChunk >> 4;
-                    tc::mma_bf16(tmem + s * 128, qd + (k >> 2) * kC + 2 * (k & 3), kd + (k >> 2) * kC + 2 * (k & 3), kIdescS,
+                    mma_ss(tmem + s * 128, qd + (k >> 2) * kC + 2 * (k & 3), kd + (k >> 2) * kC + 2 * (k & 3), kIdescS,
                                  k != 0 ? 1u : 0u);
                 }
-                tc::mma_commit(&bars->s_full[s]);
+                commit(&bars->s_full[s]);
                 in[s] = later(c, s);
                 if (!in[s]) {        // the block's last S of this sub-tile
-                    tc::mma_commit(&bars->q_empty[s]);
+                    commit(&bars->q_empty[s]);
                     ++nq[s];
                 }
             };
@@ -295,7 +310,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 ++np[s];
                 fresh[s] = !later(c, s);
                 if (fresh[s]) {
-                    tc::mma_commit(&bars->o_full[s]);
+                    commit(&bars->o_full[s]);
                     ++no[s];
                 }
             };
@@ -304,7 +319,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (active(cur, s)) issue_s(cur, s);
-                if (ok) tc::mma_commit(&bars->k_empty[cur.it % NST]);
+                if (ok) commit(&bars->k_empty[cur.it % NST]);
             }
             while (cur.valid && ok) {
                 Cursor nxt = cur;
@@ -321,12 +336,12 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     ok = tc::mbar_wait(&bars->k_full[nxt.it % NST], (nxt.it / NST) & 1, a.status);
                 if (!active(cur, 0) && !active(cur, 1))
                     ok = ok && tc::mbar_wait(&bars->v_full[cur.it % NST], (cur.it / NST) & 1, a.status);
-                if (nxt.valid) tc::mma_commit(&bars->k_empty[nxt.it % NST]);
-                tc::mma_commit(&bars->v_empty[cur.it % NST]);
+                if (nxt.valid) commit(&bars->k_empty[nxt.it % NST]);
+                commit(&bars->v_empty[cur.it % NST]);
                 cur = nxt;
             }
             if (!ok) {               // given up: the products in flight end (bounded wait) before their memory goes away
-                tc::mma_commit(&bars->drain);
+                commit(&bars->drain);
                 tc::mbar_wait(&bars->drain, 0, a.status);
             }
         }
