@@ -80,10 +80,10 @@ __device__ bool values_bad(const SwaArgs &a, int g, int64_t lo, int64_t hi, int 
     }
     return __any_sync(0xffffffffu, bad);
 }
-// Row (t, h) over exactly the keys it sees, by one warp.  Ends early once every channel is NaN, which no
+// Row (t, h) over exactly the keys it sees, by one warp; channels [d0, d1) are stored.  Ends early once every channel is NaN, which no
 // further key can change (so a sequence full of NaN does not cost a key-by-key pass per row).
 template <typename S>
-__device__ void attend_row(const SwaArgs &a, int t, int h, int lane) {
+__device__ void attend_row(const SwaArgs &a, int t, int h, int lane, int d0, int d1) {
     const int g = h / (a.H / a.Hkv);
     const S *q = (const S *)a.q + (int64_t)t * a.ld_q + (int64_t)h * a.dh;
     const S *k = (const S *)a.k + (int64_t)g * a.dh;
@@ -124,7 +124,7 @@ __device__ void attend_row(const SwaArgs &a, int t, int h, int lane) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int d = lane + 32 * i;
-        if (d < a.dh) store_val(o + d, acc[i] / l);
+        if (d >= d0 && d < d1) store_val(o + d, acc[i] / l);
     }
 }
 

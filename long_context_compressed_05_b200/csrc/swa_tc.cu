@@ -5,14 +5,15 @@
 // holds floor(128 / G) tokens.  Both sub-tiles walk the same tiles of 128 key columns (the first tokens outside the
 // window, padded to 16, then the tokens from the first row's window on; see block_keys) and share their loads.
 //   S = Q K^T        128 x 128 fp32 in TMEM, one buffer per sub-tile
-//   online softmax   a warpgroup per sub-tile, a thread per row (no exchange between threads); the running maximum is
-//                    raised, and O rescaled in TMEM, only when a row's maximum grows by more than 2^8
+//   online softmax   two warpgroups per sub-tile, two threads per row (64 columns each; they exchange the maximum through
+//                    shared memory); the running maximum is raised, and O rescaled in TMEM, only when a row's
+//                    maximum grows by more than 2^8
 //   O += P V         P (bf16) as the A operand in TMEM, written over S; V an MN-major B operand from shared memory
-// The tensor core alternates between the sub-tiles (P V of one, then its next S), so one sub-tile's products run
-// while the other's softmax does; the S of the next block is issued right behind the last P V of this one.
-// Persistent CTAs take the blocks longest first, in a snake order over the CTAs.  Warps: 0 TMA, 1 MMA, 4..7 and 8..11
-// softmax and output of sub-tile 0 and 1 (rows staged through shared memory a warp at a time, so that the stores are
-// whole 128-byte lines).
+// Each sub-tile has its own issuing warp.  They take turns, and a turn issues a P V and the next S behind it (also
+// across blocks): so one sub-tile's products run while the other's softmax does.  Without turns both sub-tiles
+// fall into step, and products and softmax take place one after the other.
+// Persistent CTAs take the blocks longest first, in a snake order over the CTAs.  Warps: 0 TMA, 1 and 2 MMA, 4..11 and
+// 12..19 softmax and output of sub-tile 0 and 1.
 //
 // Per tile of 128 x 128 at dh 128 the products take 1024 cycles of the tensor core and the exponentials 1024 of
 // the special-function unit: two equal bounds for a long window.
@@ -26,16 +27,20 @@ namespace {
 constexpr int kRows = 128;           // query rows of a sub-tile
 constexpr int kKT = 128;             // key columns of a tile
 constexpr int kGran = 16;            // rows of the small TMA boxes: padding of the first tokens' columns
-constexpr int kThreads = 384;
-// Registers a thread: 168 at launch (384 threads), shared out anew as 72 for the TMA / MMA warpgroup and 208 for
-// the two softmax warpgroups (128 x 72 + 256 x 208 <= 384 x 168)
-constexpr int kRegsIssue = 72, kRegsSoftmax = 208;
+constexpr int kHalf = kKT / 2;       // key columns of a thread
+constexpr int kGroups = kHalf / 32;
+constexpr int kThreads = 640;
+// Registers a thread: 96 at launch (640 threads), shared out anew as 64 for the TMA / MMA warpgroup and 104 for
+// the four softmax warpgroups (128 x 64 + 512 x 104 = 640 x 96)
+constexpr int kRegsIssue = 64, kRegsSoftmax = 104;
 constexpr uint32_t kColO = 256;      // TMEM: S (later P) of sub-tile s at 128 s, O at 256 + 128 s
 constexpr float kSlack = 8.f;        // exp2 units
+constexpr int kPolyOf8 = 3;          // of eight pairs of exponentials, those on the FMA pipe
 
 struct Args {
     SwaArgs a;
     int G, tb;                       // heads per key head, tokens per sub-tile
+    bool wide;                       // output rows start on 32-byte boundaries
     uint32_t blocks, n_units;        // blocks of tokens, x key heads
     float scale_log2;
 };
@@ -44,13 +49,12 @@ template <int DH> struct Sizes {
     static constexpr int kChunk = kRows * 128;              // 128 rows x 64 bf16
     static constexpr int kTile = DH / 64 * kChunk;          // Q, K or V tile
     static constexpr int kStages = DH == 128 ? 2 : 4;       // of K and of V
-    static constexpr int kStaging = 8 * 4096;               // 32 rows x 128 bytes per softmax warp
-    static constexpr int kSmem = 2 * kTile + 2 * kStages * kTile + kStaging + 2048;
+    static constexpr int kSmem = 2 * kTile + 2 * kStages * kTile + 2048;
 };
 
 template <int NST> struct Bars {
     uint64_t k_full[NST], k_empty[NST], v_full[NST], v_empty[NST];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2], drain;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], turn[2], drain[2];
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -63,7 +67,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// The issuing warp runs its loop with all lanes, so that addresses and descriptors stay in uniform registers; one
+// An issuing warp runs its loop with all lanes, so that addresses and descriptors stay in uniform registers; one
 // elected lane (always the same) issues.  With a single active lane each product cost 120 cycles to issue.
 // D[tmem] (+)= A[smem] B[smem]^T
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -86,6 +90,11 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
                  : "memory");
 }
 
+__device__ __forceinline__ void arrive_one(uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(tc::smem_u32(bar))
+                 : "memory");
+}
 __device__ __forceinline__ uint64_t f2(float x, float y) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
@@ -97,10 +106,40 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+
+// 2^x of a pair on the FMA pipe: x = n + f with n the nearest integer (by adding and subtracting 1.5 2^23), 2^f by a
+// polynomial of degree 4 fitted to the least relative error on [-1/2, 1/2] (2^-18.5, far below the 2^-9 of the
+// weights' rounding to bf16), n added to the exponent field.  x below -126 gives 2^-126.
+__device__ __forceinline__ void exp2_pair(uint64_t x, float &e0, float &e1) {
+    float x0, x1;
+    unf2(x, x0, x1);
+    x = f2(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+    const uint64_t t = add2(x, f2(12582912.f, 12582912.f));
+    const uint64_t f = add2(x, fma2(t, f2(-1.f, -1.f), f2(12582912.f, 12582912.f)));
+    uint64_t y = fma2(f, f2(0.00957010221f, 0.00957010221f), f2(0.0559178628f, 0.0559178628f));
+    y = fma2(y, f, f2(0.240247443f, 0.240247443f));
+    y = fma2(y, f, f2(0.693121791f, 0.693121791f));
+    y = fma2(y, f, f2(0.999999285f, 0.999999285f));
+    float t0, t1, y0, y1;
+    unf2(t, t0, t1);
+    unf2(y, y0, y1);
+    e0 = __int_as_float(__float_as_int(y0) + (__float_as_int(t0) << 23));
+    e1 = __int_as_float(__float_as_int(y1) + (__float_as_int(t1) << 23));
+}
+__device__ __forceinline__ void store32(void *p, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
 // Key columns of a block, the same in every role.
@@ -162,29 +201,29 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     constexpr uint32_t kIdescPV = tc::idesc_bf16(128, DH, false, true);
     const SwaArgs &a = p.a;
     extern __shared__ uint8_t smem_raw[];
+    __shared__ float exch[2][2][2][kRows];   // between the two threads of a row: slot, sub-tile, half
     Bars<NST> *bars = reinterpret_cast<Bars<NST> *>(smem_raw);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 1);
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(tmem_slot + 4) + 1023) & ~uintptr_t(1023));
-    uint8_t *staging = base + (2 + 2 * NST) * Sz::kTile;
     const uint32_t Qs = tc::smem_u32(base), Ks = Qs + 2 * Sz::kTile, Vs = Ks + NST * Sz::kTile;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
             tc::mbar_init(&bars->k_full[i], 1);
-            tc::mbar_init(&bars->k_empty[i], 1);
+            tc::mbar_init(&bars->k_empty[i], 2);   // both issuers
             tc::mbar_init(&bars->v_full[i], 1);
-            tc::mbar_init(&bars->v_empty[i], 1);
+            tc::mbar_init(&bars->v_empty[i], 2);
         }
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&bars->q_full[s], 1);
             tc::mbar_init(&bars->q_empty[s], 1);
             tc::mbar_init(&bars->s_full[s], 1);
-            tc::mbar_init(&bars->p_half[s], 4);
-            tc::mbar_init(&bars->p_full[s], 4);
+            tc::mbar_init(&bars->p_full[s], 8);
             tc::mbar_init(&bars->o_full[s], 1);
-            tc::mbar_init(&bars->o_empty[s], 4);
+            tc::mbar_init(&bars->o_empty[s], 8);
+            tc::mbar_init(&bars->turn[s], 1);
+            tc::mbar_init(&bars->drain[s], 1);
         }
-        tc::mbar_init(&bars->drain, 1);
         tc::fence_mbar_init();
     }
     if (warp == 0) tc::tmem_alloc(tmem_slot, 512);
@@ -251,109 +290,108 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     if (nq[s]) tc::mbar_wait(&bars->q_full[s], (nq[s] - 1) & 1, a.status);
             }
         }
-        } else if (warp == 1) {
-        // ---------------------------------------------------------- MMA issuer
-        {
-            uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};   // Q tiles, P tiles, blocks seen
-            bool fresh[2] = {true, true};                             // no P V of the block yet
-            struct Cursor { int k, i; uint32_t it; bool valid; Cols c; };
-            auto start = [&](int k, uint32_t it) {
-                Cursor c;
-                const int u = nth_unit(p, k);
-                c.valid = u >= 0;
-                if (c.valid) c.c = unit_of(p, u).c;
-                c.k = k;
-                c.i = 0;
-                c.it = it;
-                return c;
-            };
-            // has the block a further tile for s?  Its last one is always active
-            auto later = [&](const Cursor &c, int s) { return c.i < c.c.hi(s) / kKT; };
-            auto active = [&](const Cursor &c, int s) { return c.c.active(s, c.i); };
-            bool in[2] = {false, false};   // an S of the block has been issued
-            const uint64_t q0 = tc::sdesc_sw128(Qs, 16, 1024), k0 = tc::sdesc_sw128(Ks, 16, 1024),
+        } else if (warp <= 2) {
+            // ------------------------------------------------------ MMA issuer of sub-tile s
+            const int s = warp - 1;
+            const uint64_t qd = tc::sdesc_sw128(Qs + s * Sz::kTile, 16, 1024), k0 = tc::sdesc_sw128(Ks, 16, 1024),
                            v0 = tc::sdesc_sw128(Vs, Sz::kChunk, 1024);
-            auto issue_s = [&](const Cursor &c, int s) {
-                const int st = c.it % NST;
-                if (!in[s]) ok = ok && tc::mbar_wait(&bars->q_full[s], nq[s] & 1, a.status);
-                ok = ok && tc::mbar_wait(&bars->k_full[st], (c.it / NST) & 1, a.status);
-                if (!ok) return;
-                tc::tc_fence_after();
-                const uint64_t qd = q0 + s * (Sz::kTile >> 4), kd = k0 + st * (Sz::kTile >> 4);
-#pragma unroll
-                for (int k = 0; k < DH / 16; ++k) {
-                    constexpr int kC = Sz::kChunk >> 4;
-                    mma_ss(tmem + s * 128, qd + (k >> 2) * kC + 2 * (k & 3), kd + (k >> 2) * kC + 2 * (k & 3), kIdescS,
-                                 k != 0 ? 1u : 0u);
-                }
-                commit(&bars->s_full[s]);
-                in[s] = later(c, s);
-                if (!in[s]) {        // the block's last S of this sub-tile
-                    commit(&bars->q_empty[s]);
-                    ++nq[s];
-                }
+            const uint32_t tS = tmem + s * 128, tO = tmem + kColO + s * 128;
+            uint32_t it = 0, np = 0, nu = 0, nt = 0;   // tiles, P tiles of the sub-tile, blocks that have it, turns taken
+            auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && tc::mbar_wait(bar, parity, a.status); };
+            // The P V that the sub-tile's last tile still owes
+            bool owed = false, act = false, first = false, last = false;
+            uint32_t vst = 0, vpar = 0;
+            auto before_turn = [&]() {
+                if (!owed) return;
+                wait(&bars->v_full[vst], vpar);
+                if (!act) return;
+                if (first && nu > 1) wait(&bars->o_empty[s], nu & 1);   // of the block before this one
+                wait(&bars->p_full[s], np & 1);
             };
-            auto issue_pv = [&](const Cursor &c, int s) {
-                const int st = c.it % NST;
-                ok = ok && tc::mbar_wait(&bars->v_full[st], (c.it / NST) & 1, a.status);
-                if (fresh[s] && no[s]) ok = ok && tc::mbar_wait(&bars->o_empty[s], (no[s] - 1) & 1, a.status);
-                const uint64_t vd = v0 + st * (Sz::kTile >> 4);
+            auto issue_pv = [&]() {
+                if (owed && act) {
+                    tc::tc_fence_after();
+                    const uint64_t vd = v0 + vst * (Sz::kTile >> 4);
 #pragma unroll
-                for (int k = 0; k < kKT / 16; ++k) {
-                    if (k == 0) ok = ok && tc::mbar_wait(&bars->p_half[s], np[s] & 1, a.status);
-                    if (k == kKT / 32) ok = ok && tc::mbar_wait(&bars->p_full[s], np[s] & 1, a.status);
-                    if (!ok) return;
-                    if (k % (kKT / 32) == 0) tc::tc_fence_after();
-                    mma_ts(tmem + kColO + s * 128, tmem + s * 128 + 8 * k, vd + 128 * k, kIdescPV,
-                           !fresh[s] || k != 0 ? 1u : 0u);
+                    for (int k = 0; k < kKT / 16; ++k)
+                        mma_ts(tO, tS + 8 * k, vd + 128 * k, kIdescPV, !first || k != 0 ? 1u : 0u);
+                    ++np;
+                    if (last) commit(&bars->o_full[s]);
                 }
-                ++np[s];
-                fresh[s] = !later(c, s);
-                if (fresh[s]) {
-                    commit(&bars->o_full[s]);
-                    ++no[s];
-                }
+                if (owed) commit(&bars->v_empty[vst]);
+                owed = false;
             };
-            Cursor cur = start(0, 0);
-            if (cur.valid) {
+            auto take_turn = [&]() {
+                before_turn();
+                if (s == 1 || nt) wait(&bars->turn[s], (s == 1 ? nt : nt - 1) & 1);
+                ++nt;
+                if (ok) issue_pv();
+            };
+            for (int kk = 0; ok; ++kk) {
+                const int u = nth_unit(p, kk);
+                if (u < 0) break;
+                const Cols c = unit_of(p, u).c;
+                const int end = c.hi(s) < 0 ? -1 : c.hi(s) / kKT;   // its last tile is always active
+                bool fresh = true;
+                for (int i = 0; i < c.n_tiles; ++i, ++it) {
+                    const int st = it % NST;
+                    const uint32_t par = (it / NST) & 1;
+                    const bool now = c.active(s, i);
+                    take_turn();
+                    // waited for also where the sub-tile does not use the tile: the stage's next use is told apart by it
+                    wait(&bars->k_full[st], par);
+                    if (now && fresh) wait(&bars->q_full[s], nu & 1);
+                    if (!ok) break;
+                    if (now) {
+                        tc::tc_fence_after();
+                        const uint64_t kd = k0 + st * (Sz::kTile >> 4);
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    if (active(cur, s)) issue_s(cur, s);
-                if (ok) commit(&bars->k_empty[cur.it % NST]);
+                        for (int k = 0; k < DH / 16; ++k) {
+                            constexpr int kC = Sz::kChunk >> 4;
+                            mma_ss(tS, qd + (k >> 2) * kC + 2 * (k & 3), kd + (k >> 2) * kC + 2 * (k & 3), kIdescS,
+                                   k != 0 ? 1u : 0u);
+                        }
+                        commit(&bars->s_full[s]);
+                        if (i == end) commit(&bars->q_empty[s]);
+                        if (fresh) ++nu;
+                    }
+                    arrive_one(&bars->turn[s ^ 1]);
+                    commit(&bars->k_empty[st]);
+                    owed = true;
+                    act = now;
+                    first = fresh;
+                    last = i == end;
+                    vst = st;
+                    vpar = par;
+                    if (now) fresh = false;
+                }
             }
-            while (cur.valid && ok) {
-                Cursor nxt = cur;
-                ++nxt.it;
-                if (++nxt.i == cur.c.n_tiles) nxt = start(cur.k + 1, cur.it + 1);
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (active(cur, s)) issue_pv(cur, s);
-                    if (ok && nxt.valid && active(nxt, s)) issue_s(nxt, s);
-                }
-                if (!ok) break;
-                // K is waited for here too where no sub-tile uses it, so that its next load comes after this one
-                if (nxt.valid && !active(nxt, 0) && !active(nxt, 1))
-                    ok = tc::mbar_wait(&bars->k_full[nxt.it % NST], (nxt.it / NST) & 1, a.status);
-                if (!active(cur, 0) && !active(cur, 1))
-                    ok = ok && tc::mbar_wait(&bars->v_full[cur.it % NST], (cur.it / NST) & 1, a.status);
-                if (nxt.valid) commit(&bars->k_empty[nxt.it % NST]);
-                commit(&bars->v_empty[cur.it % NST]);
-                cur = nxt;
+            if (ok) {
+                take_turn();
+                arrive_one(&bars->turn[s ^ 1]);
             }
             if (!ok) {               // given up: the products in flight end (bounded wait) before their memory goes away
-                commit(&bars->drain);
-                tc::mbar_wait(&bars->drain, 0, a.status);
+                commit(&bars->drain[s]);
+                tc::mbar_wait(&bars->drain[s], 0, a.status);
             }
-        }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        // ---------------------------------------------------------- softmax + output (one warpgroup per sub-tile)
-        const int s = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), tS = lanes + s * 128, tO = lanes + kColO + s * 128;
+        // ---------------------------------------------------------- softmax + output
+        const int s = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t tS = lanes + s * 128 + half * kHalf, tP = lanes + s * 128 + half * (kHalf / 2),
+                       tO = lanes + kColO + s * 128 + half * (DH / 2);
+        const int pair = 1 + s * 4 + quad;                // named barrier of the two warps of these rows
         const int tl = r / p.G, hh = r - tl * p.G;
-        uint8_t *stage = staging + (warp - 4) * 4096;
         uint32_t ns = 0, nu = 0;     // S tiles and blocks seen
+        // this thread's value and the one of the row's other thread (both warps leave together where a wait failed)
+        auto swap = [&](float mine, uint32_t slot) {
+            exch[slot & 1][s][half][r] = mine;
+            ok = tc::named_bar_and(pair, 64, ok);
+            return exch[slot & 1][s][half ^ 1][r];
+        };
+        uint32_t slot = 0;
         for (int kk = 0; ok; ++kk) {
             const int u = nth_unit(p, kk);
             if (u < 0) break;
@@ -364,54 +402,66 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const int hi = row_ok ? x.hi(t) : -1, lo = row_ok ? x.lo(t, a.window) : 0;
             float m = -INFINITY, l = 0.f;
             bool first = true;
+            // tiles between these columns are seen whole by every row
+            const int clean_hi = x.hi(ta) - kKT + 1, clean_lo = x.lo(te, a.window);
             for (int i = 0; i < x.c.n_tiles; ++i) {
                 if (!x.c.active(s, i)) continue;
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->s_full[s], ns & 1, a.status));
-                if (!ok) break;
                 ++ns;
                 tc::tc_fence_after();
-                float v[kKT];
+                float v[kHalf];
 #pragma unroll
-                for (int c = 0; c < kKT; c += 32) tc::tmem_ld32(tS + c, v + c);
+                for (int c = 0; c < kHalf; c += 32) tc::tmem_ld32(tS + c, v + c);
                 tc::tmem_ld_wait();
-                const int c0 = i * kKT;
-                const bool clean = c0 + kKT - 1 <= x.hi(ta) && (c0 >= x.lo(te, a.window) || c0 + kKT <= x.c.sk);
+                // columns c0 + 32 q + c that the row sees, bit c; groups of 32 that no row of the warp sees are left out, and
+                // weigh nothing
+                const int c0 = i * kKT + half * kHalf;
+                const bool clean = i * kKT <= clean_hi && (i * kKT >= clean_lo || i * kKT + kKT <= x.c.sk);
+                unsigned groups = (1u << kGroups) - 1;
                 if (!clean) {
+                    auto upto = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
 #pragma unroll
-                    for (int q = 0; q < kKT; q += 32) {
-                        // bit c: column c0 + q + c is seen
-                        auto upto = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
-                        const int cg = c0 + q;
+                    for (int q = 0; q < kGroups; ++q) {
+                        const int cg = c0 + 32 * q;
                         const uint32_t bits = upto(hi + 1 - cg) & (~upto(lo - cg) | upto(x.c.sk - cg));
+                        if (!__any_sync(0xffffffffu, bits)) {
+                            groups &= ~(1u << q);
+                        } else if (!__all_sync(0xffffffffu, bits == ~0u)) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!(bits >> c & 1)) v[q + c] = -INFINITY;
+                            for (int c = 0; c < 32; ++c)
+                                if (!(bits >> c & 1)) v[32 * q + c] = -INFINITY;
+                        }
                     }
                 }
-                float mx[8];
+                float mt = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) mx[c] = fmaxf(v[c], v[c + 8]);
+                for (int q = 0; q < kGroups; ++q) {
+                    if (!(groups >> q & 1)) continue;
+                    float mx[4];
 #pragma unroll
-                for (int c = 16; c < kKT; c += 16)
+                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(v[32 * q + e], v[32 * q + e + 4]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) mx[e] = fmaxf(mx[e], fmaxf(v[c + e], v[c + e + 8]));
-                float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                 fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-                mt *= p.scale_log2;
+                    for (int c = 8; c < 32; c += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(v[32 * q + c + e], v[32 * q + c + e + 4]));
+                    mt = fmaxf(mt, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                }
+                mt = fmaxf(mt, swap(mt, slot++)) * p.scale_log2;
+                if (!ok) break;
                 const bool need = mt > m + kSlack;
-                if (__any_sync(0xffffffffu, need)) {
+                if (__any_sync(0xffffffffu, need)) {   // the same in both warps of the rows
                     const float m_new = need ? mt : m;
                     if (!first) {    // s_full also says that the previous P V has completed
                         const float f = need ? ex2(m - m_new) : 1.f;   // m = -inf: 0
                         l *= f;
-                        float o[32];
-#pragma unroll
-                        for (int c = 0; c < DH; c += 32) {
-                            tc::tmem_ld32(tO + c, o);
+                        float o[16];
+#pragma unroll 1
+                        for (int c = 0; c < DH / 2; c += 16) {
+                            tc::tmem_ld16(tO + c, o);
                             tc::tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= f;
-                            tc::tmem_st32(tO + c, o);
+                            for (int e = 0; e < 16; ++e) o[e] *= f;
+                            tc::tmem_st16(tO + c, o);
                         }
                     }
                     m = m_new;
@@ -419,78 +469,102 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 first = false;
                 const float ref = m == -INFINITY ? 0.f : m;   // a row that has seen no key yet: every weight 0
                 const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), ref2 = f2(-ref, -ref);
-                uint64_t sum[4] = {0, 0, 0, 0};   // pairs of zeros
+                uint64_t sum[2] = {0, 0};   // pairs of zeros
+                // part of the exponentials on the FMA pipe, where no column is masked and every row has a finite maximum
+                const bool both = clean && !__any_sync(0xffffffffu, m == -INFINITY);
 #pragma unroll
-                for (int q = 0; q < kKT; q += 64) {
-                    float w[32];
+                for (int q = 0; q < kGroups; ++q) {
+                    float w[16];
+                    if (both) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        float e0, e1;
-                        unf2(fma2(f2(v[q + 2 * c], v[q + 2 * c + 1]), sc2, ref2), e0, e1);
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
-                        sum[c & 3] = add2(sum[c & 3], f2(e0, e1));
-                        w[c] = __uint_as_float(pack2(e0, e1));
+                        for (int c = 0; c < 16; ++c) {
+                            float e0, e1;
+                            const uint64_t y = fma2(f2(v[32 * q + 2 * c], v[32 * q + 2 * c + 1]), sc2, ref2);
+                            if ((c & 7) < kPolyOf8) {
+                                exp2_pair(y, e0, e1);
+                            } else {
+                                unf2(y, e0, e1);
+                                e0 = ex2(e0);
+                                e1 = ex2(e1);
+                            }
+                            sum[c & 1] = add2(sum[c & 1], f2(e0, e1));
+                            w[c] = __uint_as_float(pack2(e0, e1));
+                        }
+                    } else if (groups >> q & 1) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            float e0, e1;
+                            unf2(fma2(f2(v[32 * q + 2 * c], v[32 * q + 2 * c + 1]), sc2, ref2), e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            sum[c & 1] = add2(sum[c & 1], f2(e0, e1));
+                            w[c] = __uint_as_float(pack2(e0, e1));
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) w[c] = 0.f;
                     }
-                    tc::tmem_st32(tS + q / 2, w);
-                    tc::tmem_st_wait();
-                    tc::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(q == 0 ? &bars->p_half[s] : &bars->p_full[s]);
+                    tc::tmem_st16(tP + 16 * q, w);
                 }
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars->p_full[s]);
                 float s0, s1;
-                unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+                unf2(add2(sum[0], sum[1]), s0, s1);
                 l += s0 + s1;
             }
             if (!ok) break;
-            // ------------------------------------------------ output
+            // ------------------------------------------------ output: half of the row's channels
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->o_full[s], nu & 1, a.status));
-            if (!ok) break;
             ++nu;
+            l += swap(l, slot++);
+            if (!ok) break;
             tc::tc_fence_after();
-            const int64_t at = row_ok ? (int64_t)t * a.ld_out + (int64_t)(x.g * p.G + hh) * DH : -1;
+            __nv_bfloat16 *dst =
+                (__nv_bfloat16 *)a.out + (int64_t)t * a.ld_out + (int64_t)(x.g * p.G + hh) * DH + half * (DH / 2);
             const float li = 1.f / l;
-            float zero = 0.f;        // NaN once an output is not finite
+            uint64_t zero = 0;       // NaN once an output is not finite
 #pragma unroll
-            for (int c = 0; c < DH; c += 64) {
-                float o[64];
+            for (int c = 0; c < DH / 2; c += 32) {
+                float o[32];
                 tc::tmem_ld32(tO + c, o);
-                tc::tmem_ld32(tO + c + 32, o + 32);
                 tc::tmem_ld_wait();
-                if (c + 64 == DH) {  // O is read
+                if (c + 32 == DH / 2) {   // O is read
                     tc::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&bars->o_empty[s]);
                 }
+                uint32_t w[16];
 #pragma unroll
-                for (int g8 = 0; g8 < 8; ++g8) {
-                    uint32_t w[4];
+                for (int e = 0; e < 16; ++e) {
+                    const uint64_t y = mul2(f2(o[2 * e], o[2 * e + 1]), f2(li, li));
+                    zero = fma2(y, 0, zero);
+                    float y0, y1;
+                    unf2(y, y0, y1);
+                    w[e] = pack2(y0, y1);
+                }
+                if (row_ok) {        // whole 32-byte sectors of the thread's own row
+                    if (p.wide) {
+                        store32(dst + c, w);
+                        store32(dst + c + 16, w + 8);
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float y0 = o[8 * g8 + 2 * e] * li, y1 = o[8 * g8 + 2 * e + 1] * li;
-                        zero = fmaf(y0, 0.f, fmaf(y1, 0.f, zero));
-                        w[e] = pack2(y0, y1);
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<uint4 *>(dst + c + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
                     }
-                    *reinterpret_cast<uint4 *>(stage + tc::sw128_offset(lane, g8)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                __syncwarp();
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {   // four rows of 128 bytes at a time
-                    const int row = 4 * q + (lane >> 3);
-                    const int64_t to = __shfl_sync(0xffffffffu, at, row);
-                    const uint4 w = *reinterpret_cast<const uint4 *>(stage + tc::sw128_offset(row, lane & 7));
-                    if (to >= 0) *reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out + to + c + 8 * (lane & 7)) = w;
-                }
-                __syncwarp();
             }
+            float z0, z1;
+            unf2(zero, z0, z1);
             // rows that are not finite: by a value that they do not see? (the columns loaded for the block)
-            for (unsigned bad = __ballot_sync(0xffffffffu, row_ok && zero != 0.f); bad; bad &= bad - 1) {
+            for (unsigned bad = __ballot_sync(0xffffffffu, row_ok && z0 + z1 != 0.f); bad; bad &= bad - 1) {
                 const int row = quad * 32 + __ffs(bad) - 1, rt = ta + row / p.G;
                 const int end = min(a.row1, x.w0 + x.c.n_tiles * kKT - x.c.pad);
                 if (values_bad<__nv_bfloat16>(a, x.g, x.w0, (int64_t)rt - a.window + 1, lane) ||
                     values_bad<__nv_bfloat16>(a, x.g, rt + 1, end, lane) ||
                     (x.c.pad && values_bad<__nv_bfloat16>(a, x.g, x.c.sk, x.c.pad, lane)))
-                    attend_row<__nv_bfloat16>(a, rt, x.g * p.G + row % p.G, lane);
+                    attend_row<__nv_bfloat16>(a, rt, x.g * p.G + row % p.G, lane, half * (DH / 2), (half + 1) * (DH / 2));
             }
         }
     }
@@ -509,6 +583,7 @@ hcsa_status launch(const SwaArgs &a, cudaStream_t st) {
     p.a = a;
     p.G = a.H / a.Hkv;
     p.tb = kRows / p.G;
+    p.wide = ((uintptr_t)a.out & 31) == 0 && a.ld_out % 16 == 0;
     p.blocks = (uint32_t)((a.row1 - a.row0 + 2 * p.tb - 1) / (2 * p.tb));
     if ((int64_t)p.blocks * a.Hkv > INT32_MAX / 2) return HCSA_ERR_UNSUPPORTED;
     p.n_units = p.blocks * a.Hkv;
