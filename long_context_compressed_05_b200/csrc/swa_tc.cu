@@ -35,7 +35,7 @@ constexpr int kThreads = 640;
 constexpr int kRegsIssue = 64, kRegsSoftmax = 104;
 constexpr uint32_t kColO = 256;      // TMEM: S (later P) of sub-tile s at 128 s, O at 256 + 128 s
 constexpr float kSlack = 8.f;        // exp2 units
-constexpr int kPolyOf8 = 3;          // of eight pairs of exponentials, those on the FMA pipe
+constexpr int kPolyOf8 = 2;          // of eight pairs of exponentials, those on the FMA pipe
 
 struct Args {
     SwaArgs a;
@@ -67,33 +67,24 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// An issuing warp runs its loop with all lanes, so that addresses and descriptors stay in uniform registers; one
-// elected lane (always the same) issues.  With a single active lane each product cost 120 cycles to issue.
-// D[tmem] (+)= A[smem] B[smem]^T
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc),
-                 "r"(accumulate)
-                 : "memory");
+// An issuing warp runs its loop with all lanes, so that addresses and descriptors stay in uniform registers (with a
+// single active lane each product cost 120 cycles to issue); the lane elected at the start issues.
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+    return r;
 }
 // D[tmem] (+)= A[tmem] B[smem]: A's row i in lane i, two bf16 per 32-bit column
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(at), "l"(bdesc), "r"(idesc),
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(at), "l"(bdesc), "r"(idesc),
                  "r"(accumulate)
                  : "memory");
 }
-// mma_commit by the elected lane
-__device__ __forceinline__ void commit(uint64_t *bar) {
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void arrive_one(uint64_t *bar) {
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(tc::smem_u32(bar))
-                 : "memory");
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 __device__ __forceinline__ uint64_t f2(float x, float y) {
     uint64_t r;
@@ -296,36 +287,35 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const uint64_t qd = tc::sdesc_sw128(Qs + s * Sz::kTile, 16, 1024), k0 = tc::sdesc_sw128(Ks, 16, 1024),
                            v0 = tc::sdesc_sw128(Vs, Sz::kChunk, 1024);
             const uint32_t tS = tmem + s * 128, tO = tmem + kColO + s * 128;
+            const bool leader = elect();
             uint32_t it = 0, np = 0, nu = 0, nt = 0;   // tiles, P tiles of the sub-tile, blocks that have it, turns taken
             auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && tc::mbar_wait(bar, parity, a.status); };
             // The P V that the sub-tile's last tile still owes
             bool owed = false, act = false, first = false, last = false;
             uint32_t vst = 0, vpar = 0;
+            // what a turn needs; P, which comes last, is waited for last
             auto before_turn = [&]() {
-                if (!owed) return;
-                wait(&bars->v_full[vst], vpar);
-                if (!act) return;
-                if (first && nu > 1) wait(&bars->o_empty[s], nu & 1);   // of the block before this one
-                wait(&bars->p_full[s], np & 1);
-            };
-            auto issue_pv = [&]() {
-                if (owed && act) {
-                    tc::tc_fence_after();
-                    const uint64_t vd = v0 + vst * (Sz::kTile >> 4);
-#pragma unroll
-                    for (int k = 0; k < kKT / 16; ++k)
-                        mma_ts(tO, tS + 8 * k, vd + 128 * k, kIdescPV, !first || k != 0 ? 1u : 0u);
-                    ++np;
-                    if (last) commit(&bars->o_full[s]);
+                if (owed) {
+                    wait(&bars->v_full[vst], vpar);
+                    if (act && first && nu > 1) wait(&bars->o_empty[s], nu & 1);   // of the block before this one
                 }
-                if (owed) commit(&bars->v_empty[vst]);
-                owed = false;
             };
             auto take_turn = [&]() {
-                before_turn();
+                if (owed && act) wait(&bars->p_full[s], np & 1);
                 if (s == 1 || nt) wait(&bars->turn[s], (s == 1 ? nt : nt - 1) & 1);
                 ++nt;
-                if (ok) issue_pv();
+                if (!ok) return;
+                tc::tc_fence_after();
+                if (owed && act) {
+                    const uint64_t vd = v0 + vst * (Sz::kTile >> 4);
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < kKT / 16; ++k)
+                            mma_ts(tO, tS + 8 * k, vd + 128 * k, kIdescPV, !first || k != 0 ? 1u : 0u);
+                        if (last) tc::mma_commit(&bars->o_full[s]);
+                    }
+                    ++np;
+                }
             };
             for (int kk = 0; ok; ++kk) {
                 const int u = nth_unit(p, kk);
@@ -337,41 +327,48 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     const int st = it % NST;
                     const uint32_t par = (it / NST) & 1;
                     const bool now = c.active(s, i);
-                    take_turn();
+                    const uint64_t kd = k0 + st * (Sz::kTile >> 4);
+                    before_turn();
                     // waited for also where the sub-tile does not use the tile: the stage's next use is told apart by it
                     wait(&bars->k_full[st], par);
                     if (now && fresh) wait(&bars->q_full[s], nu & 1);
+                    take_turn();
                     if (!ok) break;
-                    if (now) {
-                        tc::tc_fence_after();
-                        const uint64_t kd = k0 + st * (Sz::kTile >> 4);
+                    if (leader) {
+                        if (now) {
 #pragma unroll
-                        for (int k = 0; k < DH / 16; ++k) {
-                            constexpr int kC = Sz::kChunk >> 4;
-                            mma_ss(tS, qd + (k >> 2) * kC + 2 * (k & 3), kd + (k >> 2) * kC + 2 * (k & 3), kIdescS,
-                                   k != 0 ? 1u : 0u);
+                            for (int k = 0; k < DH / 16; ++k) {
+                                constexpr int kC = Sz::kChunk >> 4;
+                                tc::mma_bf16(tS, qd + (k >> 2) * kC + 2 * (k & 3), kd + (k >> 2) * kC + 2 * (k & 3), kIdescS,
+                                             k != 0 ? 1u : 0u);
+                            }
+                            tc::mma_commit(&bars->s_full[s]);
                         }
-                        commit(&bars->s_full[s]);
-                        if (i == end) commit(&bars->q_empty[s]);
-                        if (fresh) ++nu;
+                        tc::mbar_arrive(&bars->turn[s ^ 1]);
+                        if (now && i == end) tc::mma_commit(&bars->q_empty[s]);
+                        if (owed) tc::mma_commit(&bars->v_empty[vst]);
+                        tc::mma_commit(&bars->k_empty[st]);
                     }
-                    arrive_one(&bars->turn[s ^ 1]);
-                    commit(&bars->k_empty[st]);
+                    __syncwarp();
                     owed = true;
                     act = now;
                     first = fresh;
                     last = i == end;
                     vst = st;
                     vpar = par;
-                    if (now) fresh = false;
+                    if (now) {
+                        if (fresh) ++nu;
+                        fresh = false;
+                    }
                 }
             }
             if (ok) {
+                before_turn();
                 take_turn();
-                arrive_one(&bars->turn[s ^ 1]);
+                if (leader) tc::mbar_arrive(&bars->turn[s ^ 1]);
             }
             if (!ok) {               // given up: the products in flight end (bounded wait) before their memory goes away
-                commit(&bars->drain[s]);
+                if (leader) tc::mma_commit(&bars->drain[s]);
                 tc::mbar_wait(&bars->drain[s], 0, a.status);
             }
         }
@@ -384,14 +381,13 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                        tO = lanes + kColO + s * 128 + half * (DH / 2);
         const int pair = 1 + s * 4 + quad;                // named barrier of the two warps of these rows
         const int tl = r / p.G, hh = r - tl * p.G;
-        uint32_t ns = 0, nu = 0;     // S tiles and blocks seen
+        uint32_t ns = 0, nu = 0, slot = 0;   // S tiles and blocks seen, exchanges
         // this thread's value and the one of the row's other thread (both warps leave together where a wait failed)
-        auto swap = [&](float mine, uint32_t slot) {
+        auto swap = [&](float mine) {
             exch[slot & 1][s][half][r] = mine;
             ok = tc::named_bar_and(pair, 64, ok);
-            return exch[slot & 1][s][half ^ 1][r];
+            return exch[slot++ & 1][s][half ^ 1][r];
         };
-        uint32_t slot = 0;
         for (int kk = 0; ok; ++kk) {
             const int u = nth_unit(p, kk);
             if (u < 0) break;
@@ -443,13 +439,15 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
                     for (int c = 8; c < 32; c += 8)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(v[32 * q + c + e], v[32 * q + c + e + 4]));
-                    mt = fmaxf(mt, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], v[32 * q + c + e], v[32 * q + c + e + 4]);
+                    mt = max3(mt, max3(mx[0], mx[1], mx[2]), mx[3]);
                 }
-                mt = fmaxf(mt, swap(mt, slot++)) * p.scale_log2;
-                if (!ok) break;
-                const bool need = mt > m + kSlack;
-                if (__any_sync(0xffffffffu, need)) {   // the same in both warps of the rows
+                // the reference stays where no row of the two warps needs a new one (one barrier decides for both); also where
+                // a wait failed they find out together
+                if (!tc::named_bar_and(pair, 64, ok && !(mt * p.scale_log2 > m + kSlack))) {
+                    mt = fmaxf(mt, swap(mt)) * p.scale_log2;
+                    if (!ok) break;
+                    const bool need = mt > m + kSlack;
                     const float m_new = need ? mt : m;
                     if (!first) {    // s_full also says that the previous P V has completed
                         const float f = need ? ex2(m - m_new) : 1.f;   // m = -inf: 0
@@ -518,7 +516,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             // ------------------------------------------------ output: half of the row's channels
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->o_full[s], nu & 1, a.status));
             ++nu;
-            l += swap(l, slot++);
+            l += swap(l);
             if (!ok) break;
             tc::tc_fence_after();
             __nv_bfloat16 *dst =
