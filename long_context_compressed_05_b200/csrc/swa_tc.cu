@@ -67,18 +67,39 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// An issuing warp runs its loop with all lanes, so that addresses and descriptors stay in uniform registers (with a
-// single active lane each product cost 120 cycles to issue); the lane elected at the start issues.
+// An issuing warp runs its loop with all lanes and no branch around the products, so that addresses and descriptors
+// stay in uniform registers: a product takes about 30 cycles to issue, against 60 in a branch of one lane and 120
+// where one lane runs the whole loop.  `leader` is 1 in the elected lane.
 __device__ __forceinline__ uint32_t elect() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
     return r;
 }
+// D[tmem] (+)= A[smem] B[smem]^T
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc),
+                 "r"(accumulate), "r"(leader)
+                 : "memory");
+}
 // D[tmem] (+)= A[tmem] B[smem]: A's row i in lane i, two bf16 per 32-bit column
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(at), "l"(bdesc), "r"(idesc),
-                 "r"(accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t at, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(at), "l"(bdesc), "r"(idesc),
+                 "r"(accumulate), "r"(leader)
+                 : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar)),
+                 "r"(leader)
+                 : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t leader, uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(
+                     tc::smem_u32(bar)), "r"(leader)
                  : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -287,7 +308,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const uint64_t qd = tc::sdesc_sw128(Qs + s * Sz::kTile, 16, 1024), k0 = tc::sdesc_sw128(Ks, 16, 1024),
                            v0 = tc::sdesc_sw128(Vs, Sz::kChunk, 1024);
             const uint32_t tS = tmem + s * 128, tO = tmem + kColO + s * 128;
-            const bool leader = elect();
+            const uint32_t leader = elect();
             uint32_t it = 0, np = 0, nu = 0, nt = 0;   // tiles, P tiles of the sub-tile, blocks that have it, turns taken
             auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && tc::mbar_wait(bar, parity, a.status); };
             // The P V that the sub-tile's last tile still owes
@@ -308,12 +329,10 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 tc::tc_fence_after();
                 if (owed && act) {
                     const uint64_t vd = v0 + vst * (Sz::kTile >> 4);
-                    if (leader) {
 #pragma unroll
-                        for (int k = 0; k < kKT / 16; ++k)
-                            mma_ts(tO, tS + 8 * k, vd + 128 * k, kIdescPV, !first || k != 0 ? 1u : 0u);
-                        if (last) tc::mma_commit(&bars->o_full[s]);
-                    }
+                    for (int k = 0; k < kKT / 16; ++k)
+                        mma_ts(leader, tO, tS + 8 * k, vd + 128 * k, kIdescPV, !first || k != 0 ? 1u : 0u);
+                    if (last) commit(leader, &bars->o_full[s]);
                     ++np;
                 }
             };
@@ -334,22 +353,19 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     if (now && fresh) wait(&bars->q_full[s], nu & 1);
                     take_turn();
                     if (!ok) break;
-                    if (leader) {
-                        if (now) {
+                    if (now) {
 #pragma unroll
-                            for (int k = 0; k < DH / 16; ++k) {
-                                constexpr int kC = Sz::kChunk >> 4;
-                                tc::mma_bf16(tS, qd + (k >> 2) * kC + 2 * (k & 3), kd + (k >> 2) * kC + 2 * (k & 3), kIdescS,
-                                             k != 0 ? 1u : 0u);
-                            }
-                            tc::mma_commit(&bars->s_full[s]);
+                        for (int k = 0; k < DH / 16; ++k) {
+                            constexpr int kC = Sz::kChunk >> 4;
+                            mma_ss(leader, tS, qd + (k >> 2) * kC + 2 * (k & 3), kd + (k >> 2) * kC + 2 * (k & 3), kIdescS,
+                                   k != 0 ? 1u : 0u);
                         }
-                        tc::mbar_arrive(&bars->turn[s ^ 1]);
-                        if (now && i == end) tc::mma_commit(&bars->q_empty[s]);
-                        if (owed) tc::mma_commit(&bars->v_empty[vst]);
-                        tc::mma_commit(&bars->k_empty[st]);
+                        commit(leader, &bars->s_full[s]);
                     }
-                    __syncwarp();
+                    arrive(leader, &bars->turn[s ^ 1]);
+                    if (now && i == end) commit(leader, &bars->q_empty[s]);
+                    if (owed) commit(leader, &bars->v_empty[vst]);
+                    commit(leader, &bars->k_empty[st]);
                     owed = true;
                     act = now;
                     first = fresh;
@@ -365,10 +381,10 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             if (ok) {
                 before_turn();
                 take_turn();
-                if (leader) tc::mbar_arrive(&bars->turn[s ^ 1]);
+                arrive(leader, &bars->turn[s ^ 1]);
             }
             if (!ok) {               // given up: the products in flight end (bounded wait) before their memory goes away
-                if (leader) tc::mma_commit(&bars->drain[s]);
+                commit(leader, &bars->drain[s]);
                 tc::mbar_wait(&bars->drain[s], 0, a.status);
             }
         }
