@@ -4,16 +4,15 @@
 // A block is two sub-tiles of 128 query rows of one key head: a row is a (token, head of the group) pair, a sub-tile
 // holds floor(128 / G) tokens.  Both sub-tiles walk the same tiles of 128 key columns (the first tokens outside the
 // window, padded to 16, then the tokens from the first row's window on; see block_keys) and share their loads.
-//   S = Q K^T        128 x 128 fp32 in TMEM, one buffer per sub-tile
-//   online softmax   two warpgroups per sub-tile, two threads per row (64 columns each; they exchange the maximum through
-//                    shared memory); the running maximum is raised, and O rescaled in TMEM, only when a row's
-//                    maximum grows by more than 2^8
+//   S = Q K^T        steps of 64 columns, 128 x 64 fp32 in TMEM, two buffers per sub-tile: S of the next step is ready
+//                    when a step's softmax ends (with one buffer of 128 columns, which P then needs, products and
+//                    softmax of a sub-tile ran one after the other: 466 us against XX at 8192 tokens, 32 heads)
+//   online softmax   a warpgroup per sub-tile, a thread per row (no exchange between threads); the running maximum is
+//                    raised, and O rescaled in TMEM, only when a row's maximum grows by more than 2^8
 //   O += P V         P (bf16) as the A operand in TMEM, written over S; V an MN-major B operand from shared memory
-// Each sub-tile has its own issuing warp.  They take turns, and a turn issues a P V and the next S behind it (also
-// across blocks): so one sub-tile's products run while the other's softmax does.  Without turns both sub-tiles
-// fall into step, and products and softmax take place one after the other.
-// Persistent CTAs take the blocks longest first, in a snake order over the CTAs.  Warps: 0 TMA, 1 and 2 MMA, 4..11 and
-// 12..19 softmax and output of sub-tile 0 and 1.
+// Each sub-tile has its own issuing warp; the S of the next block is issued while the last steps of this one run.
+// Persistent CTAs take the blocks longest first, in a snake order over the CTAs.  Warps: 0 TMA, 1 and 2 MMA, 4..7 and
+// 8..11 softmax and output of sub-tile 0 and 1.
 //
 // Per tile of 128 x 128 at dh 128 the products take 1024 cycles of the tensor core and the exponentials 1024 of
 // the special-function unit: two equal bounds for a long window.
@@ -27,13 +26,12 @@ namespace {
 constexpr int kRows = 128;           // query rows of a sub-tile
 constexpr int kKT = 128;             // key columns of a tile
 constexpr int kGran = 16;            // rows of the small TMA boxes: padding of the first tokens' columns
-constexpr int kHalf = kKT / 2;       // key columns of a thread
-constexpr int kGroups = kHalf / 32;
-constexpr int kThreads = 640;
-// Registers a thread: 96 at launch (640 threads), shared out anew as 64 for the TMA / MMA warpgroup and 104 for
-// the four softmax warpgroups (128 x 64 + 512 x 104 = 640 x 96)
-constexpr int kRegsIssue = 64, kRegsSoftmax = 104;
-constexpr uint32_t kColO = 256;      // TMEM: S (later P) of sub-tile s at 128 s, O at 256 + 128 s
+constexpr int kHT = 64;              // key columns of a step
+constexpr int kThreads = 384;
+// Registers a thread: 168 at launch (384 threads), shared out anew as 80 for the TMA / MMA warpgroup and 208 for
+// the two softmax warpgroups (128 x 80 + 256 x 208 <= 384 x 168)
+constexpr int kRegsIssue = 80, kRegsSoftmax = 208;
+constexpr uint32_t kColO = 256;      // TMEM: S (later P) of sub-tile s at 128 s + 64 buffer, O at 256 + 128 s
 constexpr float kSlack = 8.f;        // exp2 units
 constexpr int kPolyOf8 = 2;          // of eight pairs of exponentials, those on the FMA pipe
 
@@ -54,7 +52,7 @@ template <int DH> struct Sizes {
 
 template <int NST> struct Bars {
     uint64_t k_full[NST], k_empty[NST], v_full[NST], v_empty[NST];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2], turn[2], drain[2];
+    uint64_t q_full[2], q_empty[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -95,11 +93,6 @@ __device__ __forceinline__ void commit(uint32_t leader, uint64_t *bar) {
     asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
                  "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar)),
                  "r"(leader)
-                 : "memory");
-}
-__device__ __forceinline__ void arrive(uint32_t leader, uint64_t *bar) {
-    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(
-                     tc::smem_u32(bar)), "r"(leader)
                  : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -160,10 +153,10 @@ struct Cols {
     int n_tiles;
     int hi0, hi1, lo0, lo1;          // of each sub-tile: its last column (-1: no tokens), its first window column
     __device__ __forceinline__ int hi(int s) const { return s ? hi1 : hi0; }
-    // does sub-tile s see a column of tile i?
-    __device__ __forceinline__ bool active(int s, int i) const {
-        const int c0 = i * kKT;
-        return c0 <= hi(s) && (c0 < sk || c0 + kKT - 1 >= (s ? lo1 : lo0));
+    // does sub-tile s see a column of step j (columns 64 j ..)?
+    __device__ __forceinline__ bool active(int s, int j) const {
+        const int c0 = j * kHT;
+        return c0 <= hi(s) && (c0 < sk || c0 + kHT - 1 >= (s ? lo1 : lo0));
     }
 };
 struct Unit {
@@ -209,11 +202,10 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ Args p) {
     using Sz = Sizes<DH>;
     constexpr int NST = Sz::kStages, NC = DH / 64;
-    constexpr uint32_t kIdescS = tc::idesc_bf16(128, 128, false, false);
+    constexpr uint32_t kIdescS = tc::idesc_bf16(128, kHT, false, false);
     constexpr uint32_t kIdescPV = tc::idesc_bf16(128, DH, false, true);
     const SwaArgs &a = p.a;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ float exch[2][2][2][kRows];   // between the two threads of a row: slot, sub-tile, half
     Bars<NST> *bars = reinterpret_cast<Bars<NST> *>(smem_raw);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 1);
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(tmem_slot + 4) + 1023) & ~uintptr_t(1023));
@@ -229,11 +221,13 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&bars->q_full[s], 1);
             tc::mbar_init(&bars->q_empty[s], 1);
-            tc::mbar_init(&bars->s_full[s], 1);
-            tc::mbar_init(&bars->p_full[s], 8);
+            for (int b = 0; b < 2; ++b) {
+                tc::mbar_init(&bars->s_full[s][b], 1);
+                tc::mbar_init(&bars->p_full[s][b], 4);
+            }
+            tc::mbar_init(&bars->pv_done[s], 1);
             tc::mbar_init(&bars->o_full[s], 1);
-            tc::mbar_init(&bars->o_empty[s], 8);
-            tc::mbar_init(&bars->turn[s], 1);
+            tc::mbar_init(&bars->o_empty[s], 4);
             tc::mbar_init(&bars->drain[s], 1);
         }
         tc::fence_mbar_init();
@@ -305,83 +299,96 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         } else if (warp <= 2) {
             // ------------------------------------------------------ MMA issuer of sub-tile s
             const int s = warp - 1;
+            const uint32_t leader = elect();
             const uint64_t qd = tc::sdesc_sw128(Qs + s * Sz::kTile, 16, 1024), k0 = tc::sdesc_sw128(Ks, 16, 1024),
                            v0 = tc::sdesc_sw128(Vs, Sz::kChunk, 1024);
             const uint32_t tS = tmem + s * 128, tO = tmem + kColO + s * 128;
-            const uint32_t leader = elect();
-            uint32_t it = 0, np = 0, nu = 0, nt = 0;   // tiles, P tiles of the sub-tile, blocks that have it, turns taken
+            // A walk over the steps of all blocks: S runs up to two active steps (the two buffers) ahead of P V, and less
+            // than two tiles (so that tiles the sub-tile does not use are given back in turn)
+            struct Walk {
+                int k, j, n, end;            // block, step, steps of the block, its last active one (-1: none)
+                uint32_t it, done, units;    // tiles before this one; active steps before; blocks with tokens before
+                bool fresh;                  // no active step of the block yet
+                Cols c;
+            };
+            auto enter = [&](Walk &w) {      // the block w.k
+                const int u = nth_unit(p, w.k);
+                w.j = 0;
+                w.n = 0;
+                w.fresh = true;
+                if (u < 0) return;
+                w.c = unit_of(p, u).c;
+                w.n = 2 * w.c.n_tiles;
+                w.end = w.c.hi(s) < 0 ? -1 : w.c.hi(s) / kHT;
+            };
+            auto next = [&](Walk &w, bool act) {
+                if (act) {
+                    if (w.j == w.end) ++w.units;
+                    ++w.done;
+                    w.fresh = false;
+                }
+                w.it += w.j & 1;
+                if (++w.j == w.n) {
+                    ++w.k;
+                    enter(w);
+                }
+            };
             auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && tc::mbar_wait(bar, parity, a.status); };
-            // The P V that the sub-tile's last tile still owes
-            bool owed = false, act = false, first = false, last = false;
-            uint32_t vst = 0, vpar = 0;
-            // what a turn needs; P, which comes last, is waited for last
-            auto before_turn = [&]() {
-                if (owed) {
-                    wait(&bars->v_full[vst], vpar);
-                    if (act && first && nu > 1) wait(&bars->o_empty[s], nu & 1);   // of the block before this one
-                }
-            };
-            auto take_turn = [&]() {
-                if (owed && act) wait(&bars->p_full[s], np & 1);
-                if (s == 1 || nt) wait(&bars->turn[s], (s == 1 ? nt : nt - 1) & 1);
-                ++nt;
-                if (!ok) return;
-                tc::tc_fence_after();
-                if (owed && act) {
-                    const uint64_t vd = v0 + vst * (Sz::kTile >> 4);
-#pragma unroll
-                    for (int k = 0; k < kKT / 16; ++k)
-                        mma_ts(leader, tO, tS + 8 * k, vd + 128 * k, kIdescPV, !first || k != 0 ? 1u : 0u);
-                    if (last) commit(leader, &bars->o_full[s]);
-                    ++np;
-                }
-            };
-            for (int kk = 0; ok; ++kk) {
-                const int u = nth_unit(p, kk);
-                if (u < 0) break;
-                const Cols c = unit_of(p, u).c;
-                const int end = c.hi(s) < 0 ? -1 : c.hi(s) / kKT;   // its last tile is always active
-                bool fresh = true;
-                for (int i = 0; i < c.n_tiles; ++i, ++it) {
-                    const int st = it % NST;
-                    const uint32_t par = (it / NST) & 1;
-                    const bool now = c.active(s, i);
-                    const uint64_t kd = k0 + st * (Sz::kTile >> 4);
-                    before_turn();
-                    // waited for also where the sub-tile does not use the tile: the stage's next use is told apart by it
+            auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity)); };
+            Walk ws, wp;
+            ws.k = 0;
+            ws.it = ws.done = ws.units = 0;
+            enter(ws);
+            wp = ws;
+            while (ok && wp.n) {
+                while (ok && ws.n && ws.done - wp.done < 2 && ws.it - wp.it < 2) {
+                    const int st = ws.it % NST;
+                    const uint32_t par = (ws.it / NST) & 1;
+                    const bool act = ws.c.active(s, ws.j);
+                    // where the operands are still on their way, an owed P V goes first.  K is waited for also where the
+                    // sub-tile does not use it: the stage's next use is told apart by it
+                    if (ws.done != wp.done && !(ready(&bars->k_full[st], par) &&
+                                                (!act || !ws.fresh || ready(&bars->q_full[s], ws.units & 1))))
+                        break;
                     wait(&bars->k_full[st], par);
-                    if (now && fresh) wait(&bars->q_full[s], nu & 1);
-                    take_turn();
+                    if (act && ws.fresh) wait(&bars->q_full[s], ws.units & 1);
                     if (!ok) break;
-                    if (now) {
+                    if (act) {
+                        tc::tc_fence_after();
+                        const uint32_t b = ws.done & 1;
+                        const uint64_t kd = k0 + st * (Sz::kTile >> 4) + (ws.j & 1) * (kHT * 128 >> 4);
 #pragma unroll
                         for (int k = 0; k < DH / 16; ++k) {
                             constexpr int kC = Sz::kChunk >> 4;
-                            mma_ss(leader, tS, qd + (k >> 2) * kC + 2 * (k & 3), kd + (k >> 2) * kC + 2 * (k & 3), kIdescS,
-                                   k != 0 ? 1u : 0u);
+                            mma_ss(leader, tS + b * kHT, qd + (k >> 2) * kC + 2 * (k & 3), kd + (k >> 2) * kC + 2 * (k & 3),
+                                   kIdescS, k != 0 ? 1u : 0u);
                         }
-                        commit(leader, &bars->s_full[s]);
+                        commit(leader, &bars->s_full[s][b]);
+                        if (ws.j == ws.end) commit(leader, &bars->q_empty[s]);
                     }
-                    arrive(leader, &bars->turn[s ^ 1]);
-                    if (now && i == end) commit(leader, &bars->q_empty[s]);
-                    if (owed) commit(leader, &bars->v_empty[vst]);
-                    commit(leader, &bars->k_empty[st]);
-                    owed = true;
-                    act = now;
-                    first = fresh;
-                    last = i == end;
-                    vst = st;
-                    vpar = par;
-                    if (now) {
-                        if (fresh) ++nu;
-                        fresh = false;
-                    }
+                    if (ws.j & 1) commit(leader, &bars->k_empty[st]);
+                    next(ws, act);
                 }
-            }
-            if (ok) {
-                before_turn();
-                take_turn();
-                arrive(leader, &bars->turn[s ^ 1]);
+                if (!ok) break;
+                const int st = wp.it % NST;
+                const bool act = wp.c.active(s, wp.j);
+                wait(&bars->v_full[st], (wp.it / NST) & 1);
+                if (act) {
+                    const uint32_t b = wp.done & 1;
+                    if (wp.fresh && wp.units) wait(&bars->o_empty[s], (wp.units - 1) & 1);
+                    wait(&bars->p_full[s][b], (wp.done >> 1) & 1);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const uint64_t vd = v0 + st * (Sz::kTile >> 4) + (wp.j & 1) * (kHT * 128 >> 4);
+#pragma unroll
+                    for (int k = 0; k < kHT / 16; ++k)
+                        mma_ts(leader, tO, tS + b * kHT + 8 * k, vd + 128 * k, kIdescPV, !wp.fresh || k != 0 ? 1u : 0u);
+                    commit(leader, &bars->pv_done[s]);
+                    if (wp.j == wp.end) commit(leader, &bars->o_full[s]);
+                }
+                if (!ok) break;
+                if (wp.j & 1) commit(leader, &bars->v_empty[st]);
+                next(wp, act);
             }
             if (!ok) {               // given up: the products in flight end (bounded wait) before their memory goes away
                 commit(leader, &bars->drain[s]);
@@ -390,20 +397,11 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        // ---------------------------------------------------------- softmax + output
-        const int s = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quad = warp & 3, r = quad * 32 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t tS = lanes + s * 128 + half * kHalf, tP = lanes + s * 128 + half * (kHalf / 2),
-                       tO = lanes + kColO + s * 128 + half * (DH / 2);
-        const int pair = 1 + s * 4 + quad;                // named barrier of the two warps of these rows
+        // ---------------------------------------------------------- softmax + output: a thread per row
+        const int s = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), tO = lanes + kColO + s * 128;
         const int tl = r / p.G, hh = r - tl * p.G;
-        uint32_t ns = 0, nu = 0, slot = 0;   // S tiles and blocks seen, exchanges
-        // this thread's value and the one of the row's other thread (both warps leave together where a wait failed)
-        auto swap = [&](float mine) {
-            exch[slot & 1][s][half][r] = mine;
-            ok = tc::named_bar_and(pair, 64, ok);
-            return exch[slot++ & 1][s][half ^ 1][r];
-        };
+        uint32_t ns = 0, nu = 0;     // steps and blocks seen
         for (int kk = 0; ok; ++kk) {
             const int u = nth_unit(p, kk);
             if (u < 0) break;
@@ -414,26 +412,27 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const int hi = row_ok ? x.hi(t) : -1, lo = row_ok ? x.lo(t, a.window) : 0;
             float m = -INFINITY, l = 0.f;
             bool first = true;
-            // tiles between these columns are seen whole by every row
-            const int clean_hi = x.hi(ta) - kKT + 1, clean_lo = x.lo(te, a.window);
-            for (int i = 0; i < x.c.n_tiles; ++i) {
-                if (!x.c.active(s, i)) continue;
-                ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->s_full[s], ns & 1, a.status));
-                ++ns;
+            // steps between these columns are seen whole by every row
+            const int clean_hi = x.hi(ta) - kHT + 1, clean_lo = x.lo(te, a.window), end = x.c.hi(s) / kHT;
+            for (int j = 0; j <= end; ++j) {
+                if (!x.c.active(s, j)) continue;
+                const uint32_t tS = lanes + s * 128 + (ns & 1) * kHT;
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->s_full[s][ns & 1], (ns >> 1) & 1, a.status));
+                if (!ok) break;
                 tc::tc_fence_after();
-                float v[kHalf];
-#pragma unroll
-                for (int c = 0; c < kHalf; c += 32) tc::tmem_ld32(tS + c, v + c);
+                float v[kHT];
+                tc::tmem_ld32(tS, v);
+                tc::tmem_ld32(tS + 32, v + 32);
                 tc::tmem_ld_wait();
                 // columns c0 + 32 q + c that the row sees, bit c; groups of 32 that no row of the warp sees are left out, and
                 // weigh nothing
-                const int c0 = i * kKT + half * kHalf;
-                const bool clean = i * kKT <= clean_hi && (i * kKT >= clean_lo || i * kKT + kKT <= x.c.sk);
-                unsigned groups = (1u << kGroups) - 1;
+                const int c0 = j * kHT;
+                const bool clean = c0 <= clean_hi && (c0 >= clean_lo || c0 + kHT <= x.c.sk);
+                unsigned groups = 3;
                 if (!clean) {
                     auto upto = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
 #pragma unroll
-                    for (int q = 0; q < kGroups; ++q) {
+                    for (int q = 0; q < 2; ++q) {
                         const int cg = c0 + 32 * q;
                         const uint32_t bits = upto(hi + 1 - cg) & (~upto(lo - cg) | upto(x.c.sk - cg));
                         if (!__any_sync(0xffffffffu, bits)) {
@@ -447,7 +446,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 }
                 float mt = -INFINITY;
 #pragma unroll
-                for (int q = 0; q < kGroups; ++q) {
+                for (int q = 0; q < 2; ++q) {
                     if (!(groups >> q & 1)) continue;
                     float mx[4];
 #pragma unroll
@@ -458,114 +457,114 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                         for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], v[32 * q + c + e], v[32 * q + c + e + 4]);
                     mt = max3(mt, max3(mx[0], mx[1], mx[2]), mx[3]);
                 }
-                // the reference stays where no row of the two warps needs a new one (one barrier decides for both); also where
-                // a wait failed they find out together
-                if (!tc::named_bar_and(pair, 64, ok && !(mt * p.scale_log2 > m + kSlack))) {
-                    mt = fmaxf(mt, swap(mt)) * p.scale_log2;
-                    if (!ok) break;
-                    const bool need = mt > m + kSlack;
+                mt *= p.scale_log2;
+                const bool need = mt > m + kSlack;
+                if (__any_sync(0xffffffffu, need)) {
                     const float m_new = need ? mt : m;
-                    if (!first) {    // s_full also says that the previous P V has completed
+                    if (!first) {    // O as the step before left it
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->pv_done[s], (ns - 1) & 1, a.status));
+                        if (!ok) break;
+                        tc::tc_fence_after();
                         const float f = need ? ex2(m - m_new) : 1.f;   // m = -inf: 0
                         l *= f;
-                        float o[16];
-#pragma unroll 1
-                        for (int c = 0; c < DH / 2; c += 16) {
-                            tc::tmem_ld16(tO + c, o);
+                        float o[32];
+#pragma unroll
+                        for (int c = 0; c < DH; c += 32) {
+                            tc::tmem_ld32(tO + c, o);
                             tc::tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= f;
-                            tc::tmem_st16(tO + c, o);
+                            for (int e = 0; e < 32; ++e) o[e] *= f;
+                            tc::tmem_st32(tO + c, o);
                         }
                     }
                     m = m_new;
                 }
                 first = false;
+                ++ns;
                 const float ref = m == -INFINITY ? 0.f : m;   // a row that has seen no key yet: every weight 0
                 const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), ref2 = f2(-ref, -ref);
-                uint64_t sum[2] = {0, 0};   // pairs of zeros
+                uint64_t sum[4] = {0, 0, 0, 0};   // pairs of zeros
                 // part of the exponentials on the FMA pipe, where no column is masked and every row has a finite maximum
-                const bool both = clean && !__any_sync(0xffffffffu, m == -INFINITY);
+                float w[32];
+                if (clean && !__any_sync(0xffffffffu, m == -INFINITY)) {
 #pragma unroll
-                for (int q = 0; q < kGroups; ++q) {
-                    float w[16];
-                    if (both) {
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            float e0, e1;
-                            const uint64_t y = fma2(f2(v[32 * q + 2 * c], v[32 * q + 2 * c + 1]), sc2, ref2);
-                            if ((c & 7) < kPolyOf8) {
-                                exp2_pair(y, e0, e1);
-                            } else {
-                                unf2(y, e0, e1);
-                                e0 = ex2(e0);
-                                e1 = ex2(e1);
-                            }
-                            sum[c & 1] = add2(sum[c & 1], f2(e0, e1));
-                            w[c] = __uint_as_float(pack2(e0, e1));
-                        }
-                    } else if (groups >> q & 1) {
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            float e0, e1;
-                            unf2(fma2(f2(v[32 * q + 2 * c], v[32 * q + 2 * c + 1]), sc2, ref2), e0, e1);
+                    for (int c = 0; c < 32; ++c) {
+                        float e0, e1;
+                        const uint64_t y = fma2(f2(v[2 * c], v[2 * c + 1]), sc2, ref2);
+                        if ((c & 7) < kPolyOf8) {
+                            exp2_pair(y, e0, e1);
+                        } else {
+                            unf2(y, e0, e1);
                             e0 = ex2(e0);
                             e1 = ex2(e1);
-                            sum[c & 1] = add2(sum[c & 1], f2(e0, e1));
+                        }
+                        sum[c & 3] = add2(sum[c & 3], f2(e0, e1));
+                        w[c] = __uint_as_float(pack2(e0, e1));
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                        for (int c = 16 * q; c < 16 * q + 16; ++c) w[c] = 0.f;
+                        if (!(groups >> q & 1)) continue;
+#pragma unroll
+                        for (int c = 16 * q; c < 16 * q + 16; ++c) {
+                            float e0, e1;
+                            unf2(fma2(f2(v[2 * c], v[2 * c + 1]), sc2, ref2), e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            sum[c & 3] = add2(sum[c & 3], f2(e0, e1));
                             w[c] = __uint_as_float(pack2(e0, e1));
                         }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) w[c] = 0.f;
                     }
-                    tc::tmem_st16(tP + 16 * q, w);
                 }
+                tc::tmem_st32(tS, w);
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars->p_full[s]);
+                if (lane == 0) tc::mbar_arrive(&bars->p_full[s][(ns - 1) & 1]);
                 float s0, s1;
-                unf2(add2(sum[0], sum[1]), s0, s1);
+                unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
                 l += s0 + s1;
             }
             if (!ok) break;
-            // ------------------------------------------------ output: half of the row's channels
+            // ------------------------------------------------ output
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->o_full[s], nu & 1, a.status));
-            ++nu;
-            l += swap(l);
             if (!ok) break;
+            ++nu;
             tc::tc_fence_after();
-            __nv_bfloat16 *dst =
-                (__nv_bfloat16 *)a.out + (int64_t)t * a.ld_out + (int64_t)(x.g * p.G + hh) * DH + half * (DH / 2);
+            __nv_bfloat16 *dst = (__nv_bfloat16 *)a.out + (int64_t)t * a.ld_out + (int64_t)(x.g * p.G + hh) * DH;
             const float li = 1.f / l;
             uint64_t zero = 0;       // NaN once an output is not finite
 #pragma unroll
-            for (int c = 0; c < DH / 2; c += 32) {
-                float o[32];
+            for (int c = 0; c < DH; c += 64) {
+                float o[64];
                 tc::tmem_ld32(tO + c, o);
+                tc::tmem_ld32(tO + c + 32, o + 32);
                 tc::tmem_ld_wait();
-                if (c + 32 == DH / 2) {   // O is read
+                if (c + 64 == DH) {  // O is read
                     tc::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&bars->o_empty[s]);
                 }
-                uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const uint64_t y = mul2(f2(o[2 * e], o[2 * e + 1]), f2(li, li));
-                    zero = fma2(y, 0, zero);
-                    float y0, y1;
-                    unf2(y, y0, y1);
-                    w[e] = pack2(y0, y1);
-                }
-                if (row_ok) {        // whole 32-byte sectors of the thread's own row
-                    if (p.wide) {
-                        store32(dst + c, w);
-                        store32(dst + c + 16, w + 8);
-                    } else {
+                for (int h8 = 0; h8 < 4; ++h8) {
+                    uint32_t w[8];
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<uint4 *>(dst + c + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+                    for (int e = 0; e < 8; ++e) {
+                        const uint64_t y = mul2(f2(o[16 * h8 + 2 * e], o[16 * h8 + 2 * e + 1]), f2(li, li));
+                        zero = fma2(y, 0, zero);
+                        float y0, y1;
+                        unf2(y, y0, y1);
+                        w[e] = pack2(y0, y1);
+                    }
+                    if (row_ok) {    // whole 32-byte sectors of the thread's own row
+                        if (p.wide) {
+                            store32(dst + c + 16 * h8, w);
+                        } else {
+                            *reinterpret_cast<uint4 *>(dst + c + 16 * h8) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4 *>(dst + c + 16 * h8 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
                     }
                 }
             }
@@ -574,11 +573,11 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             // rows that are not finite: by a value that they do not see? (the columns loaded for the block)
             for (unsigned bad = __ballot_sync(0xffffffffu, row_ok && z0 + z1 != 0.f); bad; bad &= bad - 1) {
                 const int row = quad * 32 + __ffs(bad) - 1, rt = ta + row / p.G;
-                const int end = min(a.row1, x.w0 + x.c.n_tiles * kKT - x.c.pad);
+                const int behind = min(a.row1, x.w0 + x.c.n_tiles * kKT - x.c.pad);
                 if (values_bad<__nv_bfloat16>(a, x.g, x.w0, (int64_t)rt - a.window + 1, lane) ||
-                    values_bad<__nv_bfloat16>(a, x.g, rt + 1, end, lane) ||
+                    values_bad<__nv_bfloat16>(a, x.g, rt + 1, behind, lane) ||
                     (x.c.pad && values_bad<__nv_bfloat16>(a, x.g, x.c.sk, x.c.pad, lane)))
-                    attend_row<__nv_bfloat16>(a, rt, x.g * p.G + row % p.G, lane, half * (DH / 2), (half + 1) * (DH / 2));
+                    attend_row<__nv_bfloat16>(a, rt, x.g * p.G + row % p.G, lane, 0, DH);
             }
         }
     }
