@@ -26,14 +26,14 @@ namespace {
 constexpr int kRows = 128;           // query rows of a sub-tile
 constexpr int kKT = 128;             // key columns of a tile
 constexpr int kGran = 16;            // rows of the small TMA boxes: padding of the first tokens' columns
-constexpr int kHT = 64;              // key columns of a step
+constexpr int kGroups = 4;           // groups of 32 key columns
+constexpr int kEarly = 3;            // of them, those whose P is handed over before the last one's is ready
 constexpr int kThreads = 384;
 // Registers a thread: 168 at launch (384 threads), shared out anew as 80 for the TMA / MMA warpgroup and 208 for
 // the two softmax warpgroups (128 x 80 + 256 x 208 <= 384 x 168)
 constexpr int kRegsIssue = 80, kRegsSoftmax = 208;
-constexpr uint32_t kColO = 256;      // TMEM: S (later P) of sub-tile s at 128 s + 64 buffer, O at 256 + 128 s
+constexpr uint32_t kColO = 256;      // TMEM: S (later P) of sub-tile s at 128 s, O at 256 + 128 s
 constexpr float kSlack = 8.f;        // exp2 units
-constexpr int kPolyOf8 = 2;          // of eight pairs of exponentials, those on the FMA pipe
 
 struct Args {
     SwaArgs a;
@@ -52,7 +52,7 @@ template <int DH> struct Sizes {
 
 template <int NST> struct Bars {
     uint64_t k_full[NST], k_empty[NST], v_full[NST], v_empty[NST];
-    uint64_t q_full[2], q_empty[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_early[2], p_full[2], o_full[2], o_empty[2], turn[2], drain[2];
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -95,6 +95,11 @@ __device__ __forceinline__ void commit(uint32_t leader, uint64_t *bar) {
                  "r"(leader)
                  : "memory");
 }
+__device__ __forceinline__ void arrive(uint32_t leader, uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(
+                     tc::smem_u32(bar)), "r"(leader)
+                 : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -122,25 +127,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// 2^x of a pair on the FMA pipe: x = n + f with n the nearest integer (by adding and subtracting 1.5 2^23), 2^f by a
-// polynomial of degree 4 fitted to the least relative error on [-1/2, 1/2] (2^-18.5, far below the 2^-9 of the
-// weights' rounding to bf16), n added to the exponent field.  x below -126 gives 2^-126.
-__device__ __forceinline__ void exp2_pair(uint64_t x, float &e0, float &e1) {
-    float x0, x1;
-    unf2(x, x0, x1);
-    x = f2(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
-    const uint64_t t = add2(x, f2(12582912.f, 12582912.f));
-    const uint64_t f = add2(x, fma2(t, f2(-1.f, -1.f), f2(12582912.f, 12582912.f)));
-    uint64_t y = fma2(f, f2(0.00957010221f, 0.00957010221f), f2(0.0559178628f, 0.0559178628f));
-    y = fma2(y, f, f2(0.240247443f, 0.240247443f));
-    y = fma2(y, f, f2(0.693121791f, 0.693121791f));
-    y = fma2(y, f, f2(0.999999285f, 0.999999285f));
-    float t0, t1, y0, y1;
-    unf2(t, t0, t1);
-    unf2(y, y0, y1);
-    e0 = __int_as_float(__float_as_int(y0) + (__float_as_int(t0) << 23));
-    e1 = __int_as_float(__float_as_int(y1) + (__float_as_int(t1) << 23));
-}
 __device__ __forceinline__ void store32(void *p, const uint32_t *w) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -153,10 +139,10 @@ struct Cols {
     int n_tiles;
     int hi0, hi1, lo0, lo1;          // of each sub-tile: its last column (-1: no tokens), its first window column
     __device__ __forceinline__ int hi(int s) const { return s ? hi1 : hi0; }
-    // does sub-tile s see a column of step j (columns 64 j ..)?
-    __device__ __forceinline__ bool active(int s, int j) const {
-        const int c0 = j * kHT;
-        return c0 <= hi(s) && (c0 < sk || c0 + kHT - 1 >= (s ? lo1 : lo0));
+    // does sub-tile s see a column of tile i?
+    __device__ __forceinline__ bool active(int s, int i) const {
+        const int c0 = i * kKT;
+        return c0 <= hi(s) && (c0 < sk || c0 + kKT - 1 >= (s ? lo1 : lo0));
     }
 };
 struct Unit {
@@ -202,7 +188,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ Args p) {
     using Sz = Sizes<DH>;
     constexpr int NST = Sz::kStages, NC = DH / 64;
-    constexpr uint32_t kIdescS = tc::idesc_bf16(128, kHT, false, false);
+    constexpr uint32_t kIdescS = tc::idesc_bf16(128, kKT, false, false);
     constexpr uint32_t kIdescPV = tc::idesc_bf16(128, DH, false, true);
     const SwaArgs &a = p.a;
     extern __shared__ uint8_t smem_raw[];
@@ -221,13 +207,12 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&bars->q_full[s], 1);
             tc::mbar_init(&bars->q_empty[s], 1);
-            for (int b = 0; b < 2; ++b) {
-                tc::mbar_init(&bars->s_full[s][b], 1);
-                tc::mbar_init(&bars->p_full[s][b], 4);
-            }
-            tc::mbar_init(&bars->pv_done[s], 1);
+            tc::mbar_init(&bars->s_full[s], 1);
+            tc::mbar_init(&bars->p_early[s], 4);
+            tc::mbar_init(&bars->p_full[s], 4);
             tc::mbar_init(&bars->o_full[s], 1);
             tc::mbar_init(&bars->o_empty[s], 4);
+            tc::mbar_init(&bars->turn[s], 1);
             tc::mbar_init(&bars->drain[s], 1);
         }
         tc::fence_mbar_init();
@@ -303,92 +288,83 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const uint64_t qd = tc::sdesc_sw128(Qs + s * Sz::kTile, 16, 1024), k0 = tc::sdesc_sw128(Ks, 16, 1024),
                            v0 = tc::sdesc_sw128(Vs, Sz::kChunk, 1024);
             const uint32_t tS = tmem + s * 128, tO = tmem + kColO + s * 128;
-            // A walk over the steps of all blocks: S runs up to two active steps (the two buffers) ahead of P V, and less
-            // than two tiles (so that tiles the sub-tile does not use are given back in turn)
-            struct Walk {
-                int k, j, n, end;            // block, step, steps of the block, its last active one (-1: none)
-                uint32_t it, done, units;    // tiles before this one; active steps before; blocks with tokens before
-                bool fresh;                  // no active step of the block yet
-                Cols c;
-            };
-            auto enter = [&](Walk &w) {      // the block w.k
-                const int u = nth_unit(p, w.k);
-                w.j = 0;
-                w.n = 0;
-                w.fresh = true;
-                if (u < 0) return;
-                w.c = unit_of(p, u).c;
-                w.n = 2 * w.c.n_tiles;
-                w.end = w.c.hi(s) < 0 ? -1 : w.c.hi(s) / kHT;
-            };
-            auto next = [&](Walk &w, bool act) {
-                if (act) {
-                    if (w.j == w.end) ++w.units;
-                    ++w.done;
-                    w.fresh = false;
-                }
-                w.it += w.j & 1;
-                if (++w.j == w.n) {
-                    ++w.k;
-                    enter(w);
-                }
-            };
+            uint32_t it = 0, np = 0, nu = 0, nt = 0;   // tiles, P tiles of the sub-tile, blocks that have it, turns taken
             auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && tc::mbar_wait(bar, parity, a.status); };
-            auto ready = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity)); };
-            Walk ws, wp;
-            ws.k = 0;
-            ws.it = ws.done = ws.units = 0;
-            enter(ws);
-            wp = ws;
-            while (ok && wp.n) {
-                while (ok && ws.n && ws.done - wp.done < 2 && ws.it - wp.it < 2) {
-                    const int st = ws.it % NST;
-                    const uint32_t par = (ws.it / NST) & 1;
-                    const bool act = ws.c.active(s, ws.j);
-                    // where the operands are still on their way, an owed P V goes first.  K is waited for also where the
-                    // sub-tile does not use it: the stage's next use is told apart by it
-                    if (ws.done != wp.done && !(ready(&bars->k_full[st], par) &&
-                                                (!act || !ws.fresh || ready(&bars->q_full[s], ws.units & 1))))
-                        break;
-                    wait(&bars->k_full[st], par);
-                    if (act && ws.fresh) wait(&bars->q_full[s], ws.units & 1);
+            // The P V that the sub-tile's last tile still owes
+            bool owed = false, act = false, first = false, last = false;
+            uint32_t vst = 0, vpar = 0;
+            auto issue_pv = [&](int from, int to, uint64_t *bar) {   // groups of keys
+                const uint64_t vd = v0 + vst * (Sz::kTile >> 4);
+                wait(bar, np & 1);
+                if (!ok) return;
+                tc::tc_fence_after();
+#pragma unroll
+                for (int k = 2 * from; k < 2 * to; ++k)
+                    mma_ts(leader, tO, tS + 8 * k, vd + 128 * k, kIdescPV, !first || k != 0 ? 1u : 0u);
+            };
+            auto before_turn = [&]() {
+                if (!owed) return;
+                wait(&bars->v_full[vst], vpar);
+                if (!act) return;
+                if (first && nu > 1) wait(&bars->o_empty[s], nu & 1);   // of the block before this one
+                issue_pv(0, kEarly, &bars->p_early[s]);
+            };
+            auto take_turn = [&]() {
+                if (s == 1 || nt) wait(&bars->turn[s], (s == 1 ? nt : nt - 1) & 1);
+                ++nt;
+                if (!ok) return;
+                if (owed && act) {
+                    issue_pv(kEarly, kGroups, &bars->p_full[s]);
+                    if (last) commit(leader, &bars->o_full[s]);
+                    ++np;
+                }
+                tc::tc_fence_after();
+            };
+            for (int kk = 0; ok; ++kk) {
+                const int u = nth_unit(p, kk);
+                if (u < 0) break;
+                const Cols c = unit_of(p, u).c;
+                const int end = c.hi(s) < 0 ? -1 : c.hi(s) / kKT;   // its last tile is always active
+                bool fresh = true;
+                for (int i = 0; i < c.n_tiles; ++i, ++it) {
+                    const int st = it % NST;
+                    const bool now = c.active(s, i);
+                    const uint64_t kd = k0 + st * (Sz::kTile >> 4);
+                    // waited for also where the sub-tile does not use the tile: the stage's next use is told apart by it
+                    wait(&bars->k_full[st], (it / NST) & 1);
+                    if (now && fresh) wait(&bars->q_full[s], nu & 1);
+                    before_turn();
+                    take_turn();
                     if (!ok) break;
-                    if (act) {
-                        tc::tc_fence_after();
-                        const uint32_t b = ws.done & 1;
-                        const uint64_t kd = k0 + st * (Sz::kTile >> 4) + (ws.j & 1) * (kHT * 128 >> 4);
+                    if (now) {
 #pragma unroll
                         for (int k = 0; k < DH / 16; ++k) {
                             constexpr int kC = Sz::kChunk >> 4;
-                            mma_ss(leader, tS + b * kHT, qd + (k >> 2) * kC + 2 * (k & 3), kd + (k >> 2) * kC + 2 * (k & 3),
-                                   kIdescS, k != 0 ? 1u : 0u);
+                            mma_ss(leader, tS, qd + (k >> 2) * kC + 2 * (k & 3), kd + (k >> 2) * kC + 2 * (k & 3), kIdescS,
+                                   k != 0 ? 1u : 0u);
                         }
-                        commit(leader, &bars->s_full[s][b]);
-                        if (ws.j == ws.end) commit(leader, &bars->q_empty[s]);
+                        commit(leader, &bars->s_full[s]);
                     }
-                    if (ws.j & 1) commit(leader, &bars->k_empty[st]);
-                    next(ws, act);
+                    arrive(leader, &bars->turn[s ^ 1]);
+                    if (now && i == end) commit(leader, &bars->q_empty[s]);
+                    if (owed) commit(leader, &bars->v_empty[vst]);
+                    commit(leader, &bars->k_empty[st]);
+                    owed = true;
+                    act = now;
+                    first = fresh;
+                    last = i == end;
+                    vst = st;
+                    vpar = (it / NST) & 1;
+                    if (now) {
+                        if (fresh) ++nu;
+                        fresh = false;
+                    }
                 }
-                if (!ok) break;
-                const int st = wp.it % NST;
-                const bool act = wp.c.active(s, wp.j);
-                wait(&bars->v_full[st], (wp.it / NST) & 1);
-                if (act) {
-                    const uint32_t b = wp.done & 1;
-                    if (wp.fresh && wp.units) wait(&bars->o_empty[s], (wp.units - 1) & 1);
-                    wait(&bars->p_full[s][b], (wp.done >> 1) & 1);
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    const uint64_t vd = v0 + st * (Sz::kTile >> 4) + (wp.j & 1) * (kHT * 128 >> 4);
-#pragma unroll
-                    for (int k = 0; k < kHT / 16; ++k)
-                        mma_ts(leader, tO, tS + b * kHT + 8 * k, vd + 128 * k, kIdescPV, !wp.fresh || k != 0 ? 1u : 0u);
-                    commit(leader, &bars->pv_done[s]);
-                    if (wp.j == wp.end) commit(leader, &bars->o_full[s]);
-                }
-                if (!ok) break;
-                if (wp.j & 1) commit(leader, &bars->v_empty[st]);
-                next(wp, act);
+            }
+            if (ok) {
+                before_turn();
+                if (ok) take_turn();
+                arrive(leader, &bars->turn[s ^ 1]);
             }
             if (!ok) {               // given up: the products in flight end (bounded wait) before their memory goes away
                 commit(leader, &bars->drain[s]);
@@ -399,7 +375,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------------------------------------------------- softmax + output: a thread per row
         const int s = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), tO = lanes + kColO + s * 128;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), tS = lanes + s * 128, tO = lanes + kColO + s * 128;
         const int tl = r / p.G, hh = r - tl * p.G;
         uint32_t ns = 0, nu = 0;     // steps and blocks seen
         for (int kk = 0; ok; ++kk) {
@@ -412,27 +388,26 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const int hi = row_ok ? x.hi(t) : -1, lo = row_ok ? x.lo(t, a.window) : 0;
             float m = -INFINITY, l = 0.f;
             bool first = true;
-            // steps between these columns are seen whole by every row
-            const int clean_hi = x.hi(ta) - kHT + 1, clean_lo = x.lo(te, a.window), end = x.c.hi(s) / kHT;
-            for (int j = 0; j <= end; ++j) {
-                if (!x.c.active(s, j)) continue;
-                const uint32_t tS = lanes + s * 128 + (ns & 1) * kHT;
-                ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->s_full[s][ns & 1], (ns >> 1) & 1, a.status));
+            // tiles between these columns are seen whole by every row
+            const int clean_hi = x.hi(ta) - kKT + 1, clean_lo = x.lo(te, a.window), end = x.c.hi(s) / kKT;
+            for (int i = 0; i <= end; ++i) {
+                if (!x.c.active(s, i)) continue;
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->s_full[s], ns & 1, a.status));
                 if (!ok) break;
                 tc::tc_fence_after();
-                float v[kHT];
-                tc::tmem_ld32(tS, v);
-                tc::tmem_ld32(tS + 32, v + 32);
+                float v[kKT];
+#pragma unroll
+                for (int c = 0; c < kKT; c += 32) tc::tmem_ld32(tS + c, v + c);
                 tc::tmem_ld_wait();
                 // columns c0 + 32 q + c that the row sees, bit c; groups of 32 that no row of the warp sees are left out, and
                 // weigh nothing
-                const int c0 = j * kHT;
-                const bool clean = c0 <= clean_hi && (c0 >= clean_lo || c0 + kHT <= x.c.sk);
-                unsigned groups = 3;
+                const int c0 = i * kKT;
+                const bool clean = c0 <= clean_hi && (c0 >= clean_lo || c0 + kKT <= x.c.sk);
+                unsigned groups = 15;
                 if (!clean) {
                     auto upto = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
+                    for (int q = 0; q < kGroups; ++q) {
                         const int cg = c0 + 32 * q;
                         const uint32_t bits = upto(hi + 1 - cg) & (~upto(lo - cg) | upto(x.c.sk - cg));
                         if (!__any_sync(0xffffffffu, bits)) {
@@ -444,10 +419,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                         }
                     }
                 }
-                float mt = -INFINITY;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (!(groups >> q & 1)) continue;
+                auto group_max = [&](int q) {
                     float mx[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) mx[e] = fmaxf(v[32 * q + e], v[32 * q + e + 4]);
@@ -455,16 +427,21 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     for (int c = 8; c < 32; c += 8)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], v[32 * q + c + e], v[32 * q + c + e + 4]);
-                    mt = max3(mt, max3(mx[0], mx[1], mx[2]), mx[3]);
+                    return max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                };
+                float mt = -INFINITY;
+                if (groups == 15) {
+                    mt = max3(group_max(0), group_max(1), fmaxf(group_max(2), group_max(3)));
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kGroups; ++q)
+                        if (groups >> q & 1) mt = fmaxf(mt, group_max(q));
                 }
                 mt *= p.scale_log2;
                 const bool need = mt > m + kSlack;
                 if (__any_sync(0xffffffffu, need)) {
                     const float m_new = need ? mt : m;
-                    if (!first) {    // O as the step before left it
-                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->pv_done[s], (ns - 1) & 1, a.status));
-                        if (!ok) break;
-                        tc::tc_fence_after();
+                    if (!first) {    // s_full also says that the previous P V has completed
                         const float f = need ? ex2(m - m_new) : 1.f;   // m = -inf: 0
                         l *= f;
                         float o[32];
@@ -484,45 +461,45 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 const float ref = m == -INFINITY ? 0.f : m;   // a row that has seen no key yet: every weight 0
                 const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), ref2 = f2(-ref, -ref);
                 uint64_t sum[4] = {0, 0, 0, 0};   // pairs of zeros
-                // part of the exponentials on the FMA pipe, where no column is masked and every row has a finite maximum
-                float w[32];
-                if (clean && !__any_sync(0xffffffffu, m == -INFINITY)) {
+                auto weigh = [&](int q, float *w) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
+                    for (int c = 0; c < 16; ++c) {
                         float e0, e1;
-                        const uint64_t y = fma2(f2(v[2 * c], v[2 * c + 1]), sc2, ref2);
-                        if ((c & 7) < kPolyOf8) {
-                            exp2_pair(y, e0, e1);
-                        } else {
-                            unf2(y, e0, e1);
-                            e0 = ex2(e0);
-                            e1 = ex2(e1);
-                        }
+                        unf2(fma2(f2(v[32 * q + 2 * c], v[32 * q + 2 * c + 1]), sc2, ref2), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
                         sum[c & 3] = add2(sum[c & 3], f2(e0, e1));
                         w[c] = __uint_as_float(pack2(e0, e1));
                     }
+                };
+                auto hand_over = [&](uint64_t *bar) {
+                    tc::tmem_st_wait();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(bar);
+                };
+                float w[16];
+                if (groups == 15) {  // without branches between the groups
+#pragma unroll
+                    for (int q = 0; q < kGroups; ++q) {
+                        weigh(q, w);
+                        tc::tmem_st16(tS + 16 * q, w);
+                        if (q == kEarly - 1) hand_over(&bars->p_early[s]);
+                    }
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
+                    for (int q = 0; q < kGroups; ++q) {
+                        if (groups >> q & 1) {
+                            weigh(q, w);
+                        } else {
 #pragma unroll
-                        for (int c = 16 * q; c < 16 * q + 16; ++c) w[c] = 0.f;
-                        if (!(groups >> q & 1)) continue;
-#pragma unroll
-                        for (int c = 16 * q; c < 16 * q + 16; ++c) {
-                            float e0, e1;
-                            unf2(fma2(f2(v[2 * c], v[2 * c + 1]), sc2, ref2), e0, e1);
-                            e0 = ex2(e0);
-                            e1 = ex2(e1);
-                            sum[c & 3] = add2(sum[c & 3], f2(e0, e1));
-                            w[c] = __uint_as_float(pack2(e0, e1));
+                            for (int c = 0; c < 16; ++c) w[c] = 0.f;
                         }
+                        tc::tmem_st16(tS + 16 * q, w);
+                        if (q == kEarly - 1) hand_over(&bars->p_early[s]);
                     }
                 }
-                tc::tmem_st32(tS, w);
-                tc::tmem_st_wait();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars->p_full[s][(ns - 1) & 1]);
+                hand_over(&bars->p_full[s]);
                 float s0, s1;
                 unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
                 l += s0 + s1;
