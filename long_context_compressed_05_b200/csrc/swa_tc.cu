@@ -11,7 +11,7 @@
 //                    raised, and O rescaled in TMEM, only when a row's maximum grows by more than 2^8
 //   O += P V         P (bf16) as the A operand in TMEM, written over S; V an MN-major B operand from shared memory
 // Each sub-tile has its own issuing warp; the S of the next block is issued while the last steps of this one run.
-// Persistent CTAs take the blocks longest first, in a snake order over the CTAs.  Warps: 0 TMA, 1 and 2 MMA, 4..7 and
+// Persistent CTAs take the blocks longest first, in a snake order over the CTAs.  Warps: 0 and 3 TMA, 1 and 2 MMA, 4..7 and
 // 8..11 softmax and output of sub-tile 0 and 1.
 //
 // Per tile of 128 x 128 at dh 128 the products take 1024 cycles of the tensor core and the exponentials 1024 of
@@ -93,6 +93,27 @@ __device__ __forceinline__ void commit(uint32_t leader, uint64_t *bar) {
     asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
                  "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar)),
                  "r"(leader)
+                 : "memory");
+}
+__device__ __forceinline__ void expect(uint32_t leader, uint64_t *bar, uint32_t bytes) {
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+                 "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(tc::smem_u32(bar)), "r"(bytes),
+                 "r"(leader)
+                 : "memory");
+}
+__device__ __forceinline__ void load_2d(uint32_t leader, uint32_t dst, const CUtensorMap *map, int c0, int c1, uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                 "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+                 "[%4];\n\t}" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(tc::smem_u32(bar)),
+                 "r"(leader)
+                 : "memory");
+}
+__device__ __forceinline__ void load_3d(uint32_t leader, uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
+                                        uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+                 "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+                 "%4}], [%5];\n\t}" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2),
+                 "r"(tc::smem_u32(bar)), "r"(leader)
                  : "memory");
 }
 __device__ __forceinline__ void arrive(uint32_t leader, uint64_t *bar) {
@@ -226,70 +247,64 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        if (warp == 0) {
-        // ---------------------------------------------------------- TMA producer
-        if (lane == 0) {
-            uint32_t it = 0, nq[2] = {0, 0}, nk = 0, nv = 0;   // tiles; loads issued
-            auto load_q = [&](const Unit &x, int s) {
-                if (x.c.hi(s) < 0) return;
-                if (nq[s]) ok = ok && tc::mbar_wait(&bars->q_empty[s], (nq[s] - 1) & 1, a.status);
+        const uint32_t leader = elect();
+        auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && tc::mbar_wait(bar, parity, a.status); };
+        if (warp == 0 || warp == 3) {
+            // ------------------------------------------------------ TMA: Q and K (warp 0), V (warp 3)
+            const bool is_v = warp == 3;
+            const CUtensorMap *map = is_v ? &tm_v : &tm_k, *map16 = is_v ? &tm_v16 : &tm_k16;
+            uint64_t *full = is_v ? bars->v_full : bars->k_full, *empty = is_v ? bars->v_empty : bars->k_empty;
+            const uint32_t ring = is_v ? Vs : Ks;
+            uint32_t it = 0, n = 0, nq0 = 0, nq1 = 0;   // tiles; loads issued
+            auto load_q = [&](const Unit &x, int s, uint32_t &nq) {
+                if (is_v || x.c.hi(s) < 0) return;
+                if (nq) wait(&bars->q_empty[s], (nq - 1) & 1);
                 if (!ok) return;
-                tc::mbar_arrive_expect_tx(&bars->q_full[s], NC * 128 * p.tb * p.G);
+                expect(leader, &bars->q_full[s], NC * 128 * p.tb * p.G);
                 for (int c = 0; c < NC; ++c)
-                    tc::tma_load_3d(Qs + s * Sz::kTile + c * Sz::kChunk, &tm_q, c * 64, x.g * p.G, x.first(s, p.tb),
-                                    &bars->q_full[s]);
-                ++nq[s];
-            };
-            auto load_kv = [&](const Unit &x, int i, bool v) {
-                uint64_t *full = v ? bars->v_full : bars->k_full, *empty = v ? bars->v_empty : bars->k_empty;
-                const int st = it % NST;
-                if (it >= NST) ok = ok && tc::mbar_wait(&empty[st], (it / NST - 1) & 1, a.status);
-                if (!ok) return;
-                const uint32_t dst = (v ? Vs : Ks) + st * Sz::kTile;
-                const int c0 = i * kKT;
-                tc::mbar_arrive_expect_tx(&full[st], Sz::kTile);
-                for (int c = 0; c < NC; ++c) {
-                    const int x0 = x.g * DH + c * 64;
-                    if (c0 >= x.c.pad) {
-                        tc::tma_load_2d(dst + c * Sz::kChunk, v ? &tm_v : &tm_k, x0, x.w0 + c0 - x.c.pad, &full[st]);
-                    } else {
-                        for (int r = 0; r < kKT; r += kGran)
-                            tc::tma_load_2d(dst + c * Sz::kChunk + r * 128, v ? &tm_v16 : &tm_k16, x0,
-                                            c0 + r < x.c.pad ? c0 + r : x.w0 + c0 + r - x.c.pad, &full[st]);
-                    }
-                }
-                ++(v ? nv : nk);
+                    load_3d(leader, Qs + s * Sz::kTile + c * Sz::kChunk, &tm_q, c * 64, x.g * p.G, x.first(s, p.tb),
+                            &bars->q_full[s]);
+                ++nq;
             };
             for (int k = 0; ok; ++k) {
                 const int u = nth_unit(p, k);
                 if (u < 0) break;
                 const Unit x = unit_of(p, u);
-                load_q(x, 0);
+                load_q(x, 0, nq0);
                 for (int i = 0; i < x.c.n_tiles && ok; ++i, ++it) {
-                    load_kv(x, i, false);
-                    if (i == 0) load_q(x, 1);
-                    if (ok) load_kv(x, i, true);
+                    const int st = it % NST, c0 = i * kKT;
+                    if (it >= NST) wait(&empty[st], (it / NST - 1) & 1);
+                    if (!ok) break;
+                    const uint32_t dst = ring + st * Sz::kTile;
+                    expect(leader, &full[st], Sz::kTile);
+                    for (int c = 0; c < NC; ++c) {
+                        const int x0 = x.g * DH + c * 64;
+                        if (c0 >= x.c.pad) {
+                            load_2d(leader, dst + c * Sz::kChunk, map, x0, x.w0 + c0 - x.c.pad, &full[st]);
+                        } else {
+                            for (int r = 0; r < kKT; r += kGran)
+                                load_2d(leader, dst + c * Sz::kChunk + r * 128, map16, x0,
+                                        c0 + r < x.c.pad ? c0 + r : x.w0 + c0 + r - x.c.pad, &full[st]);
+                        }
+                    }
+                    ++n;
+                    if (i == 0) load_q(x, 1, nq1);
                 }
             }
             // given up: the copies still in flight land (bounded waits) before the shared memory goes away
             if (!ok) {
-                for (uint32_t n = nk > NST ? nk - NST : 0; n < nk; ++n)
-                    tc::mbar_wait(&bars->k_full[n % NST], (n / NST) & 1, a.status);
-                for (uint32_t n = nv > NST ? nv - NST : 0; n < nv; ++n)
-                    tc::mbar_wait(&bars->v_full[n % NST], (n / NST) & 1, a.status);
-                for (int s = 0; s < 2; ++s)
-                    if (nq[s]) tc::mbar_wait(&bars->q_full[s], (nq[s] - 1) & 1, a.status);
+                for (uint32_t j = n > NST ? n - NST : 0; j < n; ++j)
+                    tc::mbar_wait(&full[j % NST], (j / NST) & 1, a.status);
+                if (nq0) tc::mbar_wait(&bars->q_full[0], (nq0 - 1) & 1, a.status);
+                if (nq1) tc::mbar_wait(&bars->q_full[1], (nq1 - 1) & 1, a.status);
             }
-        }
-        } else if (warp <= 2) {
+        } else {
             // ------------------------------------------------------ MMA issuer of sub-tile s
             const int s = warp - 1;
-            const uint32_t leader = elect();
             const uint64_t qd = tc::sdesc_sw128(Qs + s * Sz::kTile, 16, 1024), k0 = tc::sdesc_sw128(Ks, 16, 1024),
                            v0 = tc::sdesc_sw128(Vs, Sz::kChunk, 1024);
             const uint32_t tS = tmem + s * 128, tO = tmem + kColO + s * 128;
             uint32_t it = 0, np = 0, nu = 0, nt = 0;   // tiles, P tiles of the sub-tile, blocks that have it, turns taken
-            auto wait = [&](uint64_t *bar, uint32_t parity) { ok = ok && tc::mbar_wait(bar, parity, a.status); };
             // The P V that the sub-tile's last tile still owes
             bool owed = false, act = false, first = false, last = false;
             uint32_t vst = 0, vpar = 0;
