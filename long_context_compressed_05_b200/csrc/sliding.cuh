@@ -185,21 +185,28 @@ __device__ __forceinline__ DecodeKeys<CT> decode_keys(int pos, int window, int s
 // amax / 2^e <= 448, held to [-126, 120] so that 2^e and 2^-e are ordinary floats.
 __device__ __forceinline__ int page_exponent(float amax) {
     if (!(amax < INFINITY)) return 120;
-    const int e = lp::block_exponent(amax, 1.75f, 8);
+    if (!(amax > 0.f)) return 0;
+    // amax = m 2^k: k - 8, one more where the mantissa is above 1.75 (the sum carries into the exponent field)
+    const int e = (int)((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 135;
     return e < -126 ? -126 : e;
 }
 // 8 channels -> 8 codes of x / 2^e (e in [-126, 120]); one rounding.  At e = 120 a finite value above 248 2^120
 // would round up to 2^128, which fp32 and bf16 hold as infinity: it takes the code 240 instead (within half a step).
 __device__ __forceinline__ uint2 codes_of(const float *v, int e) {
     const float inv = lp::pow2f(-e);
-    uint32_t w[2] = {0u, 0u};
+    float t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float t = v[i] * inv;
-        if (e == 120 && fabsf(t) < INFINITY) t = fminf(fmaxf(t, -240.f), 240.f);
-        w[i >> 2] |= ((uint32_t)__nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3) & 0xFFu) << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) t[i] = v[i] * inv;
+    if (e == 120) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(t[i]) < INFINITY) t[i] = fminf(fmaxf(t[i], -240.f), 240.f);
     }
-    return make_uint2(w[0], w[1]);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(t[2 * i], t[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
 }  // namespace hcsa

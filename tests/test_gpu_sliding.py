@@ -632,3 +632,17 @@ def test_decode_fp8_exponents(h, dh, what):
     for b, x in enumerate(c.pos_h):
         h.swa_page_append(c.p, c.pages, at[:x + 1], k[:x + 1], v[:x + 1], torch.full_like(at[:x + 1], b))
     c.check(c.decode())
+
+
+def test_norm_fp8_in_place(h):
+    """x_out = x with an 8-bit output: the same codes and stream as with a buffer of its own; enough rows that some
+    have a block maximum next to a power-of-two border."""
+    rows, D = 3000, 2048
+    g = gen(51)
+    x, d, w = randn(g, rows, D), randn(g, rows, D), randn(g, D)
+    p = h.make_params(D=D)
+    y8 = [torch.empty(rows * (D + D // 32), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    xo = torch.empty_like(x)
+    h.hcsa_add_rmsnorm(p, x, d, w, 1e-6, xo, None, y8[0])
+    h.hcsa_add_rmsnorm(p, x, d, w, 1e-6, x, None, y8[1])
+    assert torch.equal(x, xo) and torch.equal(y8[0], y8[1])
