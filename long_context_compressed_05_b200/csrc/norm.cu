@@ -1,8 +1,8 @@
 // Residual addition with root-mean-square norm: s = x + delta, x_out = round(s), y = s / sqrt(mean(s^2) + eps) w,
 // y in the storage type and / or as block-scaled FP8.
 //
-// HBM-bound (about two operations per byte): each row is read once into registers (the raw vectors of x and
-// delta), reduced, and written from registers.  A row belongs to `tpr` threads of a block (a power of two);
+// HBM-bound (about two operations per byte): each row is read once into registers, reduced, and written from
+// registers.  A row belongs to `tpr` threads of a block (a power of two);
 // several rows share a block when rows are short.
 #include "sliding.cuh"
 
@@ -42,10 +42,10 @@ __device__ __forceinline__ T row_sum(T v, int tpr, int sub, T *red) {
     return v;
 }
 
-// The sum of squares is fp32: a thread's at most 64 values (in eight partial sums), then a tree of at most 10: y is
+// The sum of squares is fp32: a thread's at most 32 values (in eight partial sums), then a tree of at most 10: y is
 // within 2^-19 of its exact value.  FP8: a block whose maximum lies within 2^-18 of a power-of-two border makes its
 // row sum once more in fp64 and takes the border's side from that; one row in a thousand has such a block.  (With
-// every sum in fp64, 131072 rows of 2048 took 778 us instead of XX.)
+// every sum in fp64, 131072 rows of 2048 took 778 us instead of 334.)
 // The row's 1 / sqrt(mean + eps) in fp64, read again (out of line: it would double the kernel's registers).
 template <typename S>
 __device__ __noinline__ double exact_rstd(const NormArgs &a, int64_t row, bool live, int tid, int tpr, int sub, double *red) {
@@ -90,8 +90,17 @@ __device__ __noinline__ void exact_blocks(const NormArgs &a, int64_t row, bool l
     }
 }
 
+// lp::block_amax where the whole warp calls it (a partial mask costs a warp synchronisation per shuffle)
+__device__ __forceinline__ float warp_block_amax(const float *v) {
+    float a = fmaxf(fabsf(v[0]), fabsf(v[1]));
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) a = fmaxf(a, fmaxf(fabsf(v[i]), fabsf(v[i + 1])));
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    return fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+}
+
 template <typename S, int VPT, bool FP8>
-__global__ void __launch_bounds__(VPT == 8 ? 256 : 1024, VPT == 8 ? 2 : 1) add_rmsnorm_kernel(NormArgs a, int tpr) {
+__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(NormArgs a, int tpr) {
     using R = Row<S>;
     constexpr int V = R::V;
     __shared__ float red[32];
@@ -154,7 +163,7 @@ __global__ void __launch_bounds__(VPT == 8 ? 256 : 1024, VPT == 8 ? 2 : 1) add_r
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {   // D % 32 == 0: the four lanes of a block are in or out together
             const int c = tid + i * tpr;
-            const float amax = lp::block_amax(v[i]);
+            const float amax = warp_block_amax(v[i]);
             const int e = page_exponent(amax);
             const float f = amax * lp::pow2f(-e);   // (224, 448] unless held or zero
             near |= f > 448.f - 448.f * 0x1p-18f || fabsf(f - 224.f) < 224.f * 0x1p-18f;
@@ -179,15 +188,14 @@ __global__ void __launch_bounds__(VPT == 8 ? 256 : 1024, VPT == 8 ? 2 : 1) add_r
 
 template <typename S, int VPT, bool FP8>
 void launch(const NormArgs &a, int tpr, cudaStream_t st) {
-    const int threads = tpr > 256 ? tpr : 256, per = threads / tpr;
+    const int threads = tpr > 128 ? tpr : 128, per = threads / tpr;
     add_rmsnorm_kernel<S, VPT, FP8><<<(unsigned)((a.rows + per - 1) / per), threads, 0, st>>>(a, tpr);
 }
 template <typename S, bool FP8>
 void launch_v(const NormArgs &a, int vpt, int tpr, cudaStream_t st) {
     if (vpt == 1) launch<S, 1, FP8>(a, tpr, st);
     else if (vpt == 2) launch<S, 2, FP8>(a, tpr, st);
-    else if (vpt == 4) launch<S, 4, FP8>(a, tpr, st);
-    else launch<S, 8, FP8>(a, tpr, st);
+    else launch<S, 4, FP8>(a, tpr, st);
 }
 
 }  // namespace
@@ -195,13 +203,10 @@ void launch_v(const NormArgs &a, int vpt, int tpr, cudaStream_t st) {
 hcsa_status launch_add_rmsnorm(const NormArgs &a, cudaStream_t st) {
     if (a.rows == 0) return HCSA_OK;
     const int nvec = a.D / (a.dtype == HCSA_BF16 ? 8 : 4);
-    // few rows: one vector per thread (the shortest path); many: up to eight, so that a row of 2048 bf16 is one warp's
-    // and needs no barrier
+    // few rows: one vector per thread (the shortest path); many: up to four (131072 rows of 2048, FP8: 334 us; 537 with
+    // two, more threads to reduce over; 406 with eight, fewer warps per SM)
     int vpt = 1;
-    if (a.rows > 1024)
-        while (vpt < 8 && vpt * 32 < nvec) vpt *= 2;
-    while (vpt < 8 && (nvec + vpt - 1) / vpt > 1024) vpt *= 2;
-    if (vpt == 8 && nvec > 8 * 256) vpt = 4;   // blocks of 256 threads hold rows of up to 2048 vectors
+    while (vpt < 4 && ((a.rows > 1024 && vpt * 32 < nvec) || vpt * 1024 < nvec)) vpt *= 2;
     int tpr = 32;
     while (tpr < (nvec + vpt - 1) / vpt) tpr *= 2;
     if (a.dtype == HCSA_F32) launch_v<float, false>(a, vpt, tpr, st);

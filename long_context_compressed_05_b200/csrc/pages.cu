@@ -1,53 +1,82 @@
 // Paged key / value cache: new tokens' rows into the pages, in the storage type or as block-scaled FP8.
-// Bandwidth- or launch-bound: one thread per 16-byte vector of the sources, no shared state.
+// Bandwidth- or launch-bound.  A block takes up to kRows rows: one thread per row finds where it goes (position, page,
+// bounds), then the block copies the rows' 16-byte vectors, four a thread in flight.
 #include "sliding.cuh"
 
 namespace hcsa {
 
 namespace {
 
-// nv: 16-byte vectors of one row's heads (Hkv dh / VEC); threads 0 .. nv - 1 of a row take k, the rest v
+constexpr int kRows = 32, kThreads = 256;
+
+// nv: 16-byte vectors of one row's heads (Hkv dh / VEC): vectors 0 .. nv - 1 of a row are k's, the next nv v's
 template <typename S, bool FP8>
-__global__ void __launch_bounds__(256) page_append_kernel(PageArgs a, int64_t rows, int nv, const int32_t *pos,
-                                                          const int32_t *seq, const S *k, int64_t ld_k, const S *v,
-                                                          int64_t ld_v) {
+__global__ void __launch_bounds__(kThreads)
+page_append_kernel(PageArgs a, int64_t rows, int per_block, int nv, const int32_t *pos, const int32_t *seq, const S *k,
+                   int64_t ld_k, const S *v, int64_t ld_v) {
     constexpr int V = Traits<S>::VEC;
-    const int64_t total = rows * 2 * nv;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t r = i / (2 * nv);
-        int c = (int)(i - r * 2 * nv);
-        const bool is_v = c >= nv;
-        if (is_v) c -= nv;
+    __shared__ int sm_line[kRows];   // row of head 0 in the page arrays, -1: the row is skipped
+    const int64_t r0 = (int64_t)blockIdx.x * per_block;
+    const int n = rows - r0 < per_block ? (int)(rows - r0) : per_block;
+    if (threadIdx.x < n) {
+        const int64_t r = r0 + threadIdx.x;
         const int p = pos[r];
         const int64_t b = seq ? seq[r] : r;
-        if (p < 0 || b < 0) continue;
-        if (b >= a.B || p >= (int64_t)a.max_pages * a.page) {
-            report(a.status, kStatusBounds);
-            continue;
+        int line = -1;
+        if (p >= 0 && b >= 0) {
+            int id = -1;
+            if (b < a.B && p < (int64_t)a.max_pages * a.page) id = a.table[b * a.max_pages + p / a.page];
+            if (id < 0 || id >= a.n_pages) report(a.status, kStatusBounds);
+            else line = id * a.Hkv * a.page + p % a.page;   // below 2^31 (checked on the host)
         }
-        const int id = a.table[b * a.max_pages + p / a.page];
-        if (id < 0 || id >= a.n_pages) {
-            report(a.status, kStatusBounds);
-            continue;
-        }
-        const int g = c * V / a.dh, d = c * V - g * a.dh;
-        const int64_t line = ((int64_t)id * a.Hkv + g) * a.page + p % a.page;
-        const uint4 raw = __ldg(reinterpret_cast<const uint4 *>((is_v ? v + r * ld_v : k + r * ld_k) + c * V));
-        void *dst = is_v ? a.v_pages : a.k_pages;
-        if constexpr (!FP8) {
-            *reinterpret_cast<uint4 *>((S *)dst + line * a.dh + d) = raw;
-        } else {
-            // the four threads of a 32-channel block are four consecutive lanes: 2 nv and the block size are
-            // multiples of 4, so they share the row and leave the loop together
-            float x[V];
-            const S *e = reinterpret_cast<const S *>(&raw);
+        sm_line[threadIdx.x] = line;
+    }
+    __syncthreads();
+    const unsigned per_row = 2u * nv, total = n * per_row;   // per_row is at most 2^24, n > 1 only where it is small
+    for (unsigned base = 0; base < total; base += 4 * kThreads) {
+        uint4 raw[4];
+        int line[4], at[4];
+        bool is_v[4];
 #pragma unroll
-            for (int q = 0; q < V; ++q) x[q] = (float)e[q];
-            const int ex = page_exponent(lp::block_amax(x));
-            uint8_t *codes = (uint8_t *)dst;
-            *reinterpret_cast<uint2 *>(codes + line * a.dh + d) = codes_of(x, ex);
-            if ((d & 31) == 0)
-                ((int8_t *)codes)[(int64_t)a.n_pages * a.Hkv * a.page * a.dh + line * (a.dh / 32) + d / 32] = (int8_t)ex;
+        for (int j = 0; j < 4; ++j) {
+            const unsigned i = base + j * kThreads + threadIdx.x;
+            const unsigned r = i / per_row;
+            unsigned c = i - r * per_row;
+            is_v[j] = c >= (unsigned)nv;
+            if (is_v[j]) c -= nv;
+            line[j] = i < total ? sm_line[r] : -1;
+            at[j] = (int)c * V;
+            raw[j] = make_uint4(0, 0, 0, 0);
+            if (line[j] >= 0)
+                raw[j] = __ldg(reinterpret_cast<const uint4 *>(
+                    (is_v[j] ? v + (r0 + r) * ld_v : k + (r0 + r) * ld_k) + at[j]));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int g = at[j] / a.dh, d = at[j] - g * a.dh;
+            const int64_t to = (int64_t)line[j] + (int64_t)g * a.page;
+            void *dst = is_v[j] ? a.v_pages : a.k_pages;
+            if constexpr (!FP8) {
+                if (line[j] >= 0) *reinterpret_cast<uint4 *>((S *)dst + to * a.dh + d) = raw[j];
+            } else {
+                // the four threads of a 32-channel block are consecutive lanes of one row; the whole warp shuffles
+                float x[V];
+                const S *e = reinterpret_cast<const S *>(&raw[j]);
+#pragma unroll
+                for (int q = 0; q < V; ++q) x[q] = (float)e[q];
+                float amax = 0.f;
+#pragma unroll
+                for (int q = 0; q < V; ++q) amax = fmaxf(amax, fabsf(x[q]));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                if (line[j] >= 0) {
+                    const int ex = page_exponent(amax);
+                    uint8_t *codes = (uint8_t *)dst;
+                    *reinterpret_cast<uint2 *>(codes + to * a.dh + d) = codes_of(x, ex);
+                    if ((d & 31) == 0)
+                        ((int8_t *)codes)[(int64_t)a.n_pages * a.Hkv * a.page * a.dh + to * (a.dh / 32) + d / 32] = (int8_t)ex;
+                }
+            }
         }
     }
 }
@@ -57,17 +86,27 @@ __global__ void __launch_bounds__(256) page_append_kernel(PageArgs a, int64_t ro
 hcsa_status launch_page_append(const PageArgs &a, int64_t rows, const int32_t *pos, const int32_t *seq, const void *k,
                                int64_t ld_k, const void *v, int64_t ld_v, cudaStream_t st) {
     if (rows == 0) return HCSA_OK;
-    const int nv = a.Hkv * a.dh / (a.dtype == HCSA_BF16 ? 8 : 4);
-    const int64_t blocks = (rows * 2 * nv + 255) / 256;
-    const unsigned grid = (unsigned)(blocks < (1 << 30) ? blocks : (1 << 30));
+    const int64_t nv64 = (int64_t)a.Hkv * a.dh / (a.dtype == HCSA_BF16 ? 8 : 4);
+    if (nv64 > 1 << 23) return HCSA_ERR_UNSUPPORTED;
+    const int nv = (int)nv64;
+    // rows per block: about a thousand vectors, fewer where the blocks would not fill the GPU
+    int64_t per = 1024 / (2 * nv);
+    const int64_t spread = rows / (4 * sm_grid(1));
+    if (per > spread) per = spread;
+    if (per > kRows) per = kRows;
+    if (per < 1) per = 1;
+    const int64_t blocks = (rows + per - 1) / per;
+    if (blocks > INT32_MAX) return HCSA_ERR_UNSUPPORTED;
+    const unsigned grid = (unsigned)blocks, threads = kThreads;
+    const int rpb = (int)per;
     if (a.dtype == HCSA_F32)
-        page_append_kernel<float, false><<<grid, 256, 0, st>>>(a, rows, nv, pos, seq, (const float *)k, ld_k,
+        page_append_kernel<float, false><<<grid, threads, 0, st>>>(a, rows, rpb, nv, pos, seq, (const float *)k, ld_k,
                                                                (const float *)v, ld_v);
     else if (a.lowprec)
-        page_append_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(a, rows, nv, pos, seq, (const __nv_bfloat16 *)k,
+        page_append_kernel<__nv_bfloat16, true><<<grid, threads, 0, st>>>(a, rows, rpb, nv, pos, seq, (const __nv_bfloat16 *)k,
                                                                       ld_k, (const __nv_bfloat16 *)v, ld_v);
     else
-        page_append_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(a, rows, nv, pos, seq, (const __nv_bfloat16 *)k,
+        page_append_kernel<__nv_bfloat16, false><<<grid, threads, 0, st>>>(a, rows, rpb, nv, pos, seq, (const __nv_bfloat16 *)k,
                                                                        ld_k, (const __nv_bfloat16 *)v, ld_v);
     count_launch();
     return check_launch();
