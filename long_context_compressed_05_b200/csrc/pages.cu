@@ -31,11 +31,10 @@ page_append_kernel(PageArgs a, int64_t rows, int per_block, int nv, const int32_
         }
         sm_line[threadIdx.x] = line;
     }
-    __syncthreads();
     const unsigned per_row = 2u * nv, total = n * per_row;   // per_row is at most 2^24, n > 1 only where it is small
     for (unsigned base = 0; base < total; base += 4 * kThreads) {
         uint4 raw[4];
-        int line[4], at[4];
+        int row[4], at[4];
         bool is_v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -44,13 +43,17 @@ page_append_kernel(PageArgs a, int64_t rows, int per_block, int nv, const int32_
             unsigned c = i - r * per_row;
             is_v[j] = c >= (unsigned)nv;
             if (is_v[j]) c -= nv;
-            line[j] = i < total ? sm_line[r] : -1;
+            row[j] = (int)r;
             at[j] = (int)c * V;
             raw[j] = make_uint4(0, 0, 0, 0);
-            if (line[j] >= 0)
+            if (i < total)
                 raw[j] = __ldg(reinterpret_cast<const uint4 *>(
                     (is_v[j] ? v + (r0 + r) * ld_v : k + (r0 + r) * ld_k) + at[j]));
         }
+        if (base == 0) __syncthreads();   // the rows' places, looked up while the first loads run
+        int line[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) line[j] = row[j] < n ? sm_line[row[j]] : -1;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int g = at[j] / a.dh, d = at[j] - g * a.dh;
