@@ -329,50 +329,63 @@ def make_pages(k_pages, v_pages, page_table) -> Pages:
         raise HcsaError("make_pages", 2)
     pages = Pages(k_pages=_ptr(k_pages), v_pages=_ptr(v_pages), page_table=_ptr(page_table))
     pages.tensors = (k_pages, v_pages, page_table)
+    # what the calls check: element type, bytes of the smaller array, entries of the table, device
+    pages.dtype = k_pages.dtype if k_pages.dtype == v_pages.dtype else None
+    pages.bytes = min(t.numel() * t.element_size() for t in (k_pages, v_pages))
+    pages.entries = page_table.numel()
+    dev = {t.get_device() for t in pages.tensors}
+    pages.device = dev.pop() if len(dev) == 1 else -1
     return pages
 
 
+# These calls check what the C library cannot see (element types, extents, strides, devices).  A decode step makes many
+# of them, so the checks are few attribute reads each and the stream comes from torch's raw accessors: about
+# 9 us a call on the host instead of 15, the launch included.
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _rows2d(fn, t, dtype, rows, cols):
-    """A [rows, cols] tensor of the call's type whose columns are contiguous (what the C call cannot see); a
-    single row's stride does not matter.  Returns its leading dimension."""
-    if t.dtype != dtype:
+    """A [rows, cols] tensor of the call's type whose columns are contiguous; a single row's stride does not matter.
+    Returns its leading dimension."""
+    if t.dtype is not dtype:
         raise HcsaError(fn, 3)
-    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < rows or shape[1] != cols or (stride[1] != 1 and cols > 1):
         raise HcsaError(fn, 2)
-    return t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0))
+    return stride[0] if shape[0] > 1 else max(cols, stride[0])
 
 
 def _vec32(fn, t, n):
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise HcsaError(fn, 3)
     if t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
         raise HcsaError(fn, 2)
 
 
 def _check_pages(fn, p, pages):
-    k, v, table = pages.tensors
-    need = int(load().hcsa_page_bytes(ctypes.byref(p)))
     dt = torch.uint8 if p.lowprec else _TORCH.get(p.dtype)
-    if k.dtype != dt or v.dtype != dt:
+    if pages.dtype is not dt:
         raise HcsaError(fn, 3)
-    if (k.numel() * k.element_size() < need or v.numel() * v.element_size() < need
-            or table.numel() < p.B * p.max_pages):
+    rows, dh = p.n_pages * p.Hkv * p.page, p.dh
+    if (pages.bytes < rows * (dh + dh // 32 if p.lowprec else dh * dt.itemsize)
+            or pages.entries < p.B * p.max_pages):
         raise HcsaError(fn, 2)
 
 
-class _on:
-    """The device of a call's tensors as the current one (they may live on another)."""
-
-    def __init__(self, t):
-        self.guard = torch.cuda.device(t.device) if t.is_cuda and t.device.index != torch.cuda.current_device() else None
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+def _call(fn, dev, stream, tensors, call, *args):
+    """The call on the tensors' device (which need not be the current one); its stream there unless one is given."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise HcsaError(fn, 2)
+    if dev < 0:
+        raise HcsaError(fn, 2)
+    if dev == _current_device():
+        code = call(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = call(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        raise HcsaError(fn, code)
 
 
 def hcsa_page_bytes(p: Params) -> int:
@@ -381,47 +394,48 @@ def hcsa_page_bytes(p: Params) -> int:
 
 def swa_attend(p, q, k, v, out, stream=None):
     """q, out: [T, H * dh]; k, v: [T, Hkv * dh] (column views of one projection are fine)."""
-    dt, n, nkv = _TORCH.get(p.dtype), p.H * p.dh, p.Hkv * p.dh
-    ld = [_rows2d("swa_attend", t, dt, p.T, c) for t, c in ((q, n), (k, nkv), (v, nkv), (out, n))]
-    with _on(q):
-        _check("swa_attend", load().swa_attend(ctypes.byref(p), _ptr(q), ld[0], _ptr(k), ld[1], _ptr(v), ld[2],
-                                               _ptr(out), ld[3], _stream(stream)))
+    fn, dt, T, dh = "swa_attend", _TORCH.get(p.dtype), p.T, p.dh
+    n, nkv = p.H * dh, p.Hkv * dh
+    lq, lk, lv, lo = _rows2d(fn, q, dt, T, n), _rows2d(fn, k, dt, T, nkv), _rows2d(fn, v, dt, T, nkv), \
+        _rows2d(fn, out, dt, T, n)
+    _call(fn, q.get_device(), stream, (k, v, out), load().swa_attend, ctypes.byref(p), q.data_ptr(), lq, k.data_ptr(),
+          lk, v.data_ptr(), lv, out.data_ptr(), lo)
 
 
 def swa_page_append(p, pages: Pages, pos, k, v, seq=None, stream=None):
     """Write k, v [rows, Hkv * dh] to tokens pos[r] of sequences seq[r] (default: sequence r); pos[r] < 0: skipped."""
     fn, dt, nkv, rows = "swa_page_append", _TORCH.get(p.dtype), p.Hkv * p.dh, k.shape[0]
-    ld = [_rows2d(fn, t, dt, rows, nkv) for t in (k, v)]
+    lk, lv = _rows2d(fn, k, dt, rows, nkv), _rows2d(fn, v, dt, rows, nkv)
     _vec32(fn, pos, rows)
     if seq is not None:
         _vec32(fn, seq, rows)
     _check_pages(fn, p, pages)
-    with _on(k):
-        _check(fn, load().swa_page_append(ctypes.byref(p), ctypes.byref(pages), rows, _ptr(pos), _ptr(seq), _ptr(k),
-                                          ld[0], _ptr(v), ld[1], _stream(stream)))
+    _call(fn, pages.device, stream, (k, v, pos, seq), load().swa_page_append, ctypes.byref(p), ctypes.byref(pages), rows,
+          pos.data_ptr(), _ptr(seq), k.data_ptr(), lk, v.data_ptr(), lv)
 
 
 def swa_decode_attend(p, pages: Pages, pos, q, out, ws=None, stream=None):
     """q, out: [B, H * dh]; pos[b]: position of the new token (already in the pages), -1 for an empty slot."""
-    fn, dt, n = "swa_decode_attend", _TORCH.get(p.dtype), p.H * p.dh
-    ld = [_rows2d(fn, t, dt, p.B, n) for t in (q, out)]
-    _vec32(fn, pos, p.B)
+    fn, dt, n, B = "swa_decode_attend", _TORCH.get(p.dtype), p.H * p.dh, p.B
+    lq, lo = _rows2d(fn, q, dt, B, n), _rows2d(fn, out, dt, B, n)
+    _vec32(fn, pos, B)
     _check_pages(fn, p, pages)
-    with _on(q):
-        _check(fn, load().swa_decode_attend(ctypes.byref(p), ctypes.byref(pages), _ptr(pos), _ptr(q), ld[0], _ptr(out),
-                                            ld[1], _ptr(ws), _wsz(ws), _stream(stream)))
+    _call(fn, pages.device, stream, (q, out, pos, ws), load().swa_decode_attend, ctypes.byref(p), ctypes.byref(pages),
+          pos.data_ptr(), q.data_ptr(), lq, out.data_ptr(), lo, _ptr(ws), _wsz(ws))
 
 
 def hcsa_add_rmsnorm(p, x, delta, w, eps, x_out, y, y8=None, stream=None):
     """x_out = x + delta, y = rmsnorm(x + delta) * w ([rows, D]); delta, x_out, y or y8 (a byte buffer of
     rows * (D + D / 32), FP8 layout) may be None."""
     fn, dt, D, rows = "hcsa_add_rmsnorm", _TORCH.get(p.dtype), p.D, x.shape[0]
-    ld = [0 if t is None else _rows2d(fn, t, dt, rows, D) for t in (x, delta, x_out, y)]
-    if w.dtype != dt or (y8 is not None and y8.dtype != torch.uint8):
+    lx = _rows2d(fn, x, dt, rows, D)
+    ld = 0 if delta is None else _rows2d(fn, delta, dt, rows, D)
+    lo = 0 if x_out is None else _rows2d(fn, x_out, dt, rows, D)
+    ly = 0 if y is None else _rows2d(fn, y, dt, rows, D)
+    if w.dtype is not dt or (y8 is not None and y8.dtype is not torch.uint8):
         raise HcsaError(fn, 3)
-    if w.shape != (D,) or not w.is_contiguous() or (
+    if w.dim() != 1 or w.shape[0] != D or not w.is_contiguous() or (
             y8 is not None and (y8.numel() < rows * (D + D // 32) or not y8.is_contiguous())):
         raise HcsaError(fn, 2)
-    with _on(x):
-        _check(fn, load().hcsa_add_rmsnorm(ctypes.byref(p), rows, _ptr(x), ld[0], _ptr(delta), ld[1], _ptr(w), eps,
-                                           _ptr(x_out), ld[2], _ptr(y), ld[3], _ptr(y8), _stream(stream)))
+    _call(fn, x.get_device(), stream, (delta, w, x_out, y, y8), load().hcsa_add_rmsnorm, ctypes.byref(p), rows,
+          x.data_ptr(), lx, _ptr(delta), ld, w.data_ptr(), eps, _ptr(x_out), lo, _ptr(y), ly, _ptr(y8))

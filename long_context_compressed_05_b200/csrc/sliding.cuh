@@ -42,6 +42,8 @@ hcsa_status launch_swa_simt(const SwaArgs &a, cudaStream_t st);
 bool swa_tc_supported(const SwaArgs &a);                          // bf16, dh 64 or 128, a positive scale
 hcsa_status launch_swa_tc(const SwaArgs &a, cudaStream_t st);
 int sm_grid(int per_sm);                                      // SMs of the device x per_sm
+// Opt in to `bytes` of dynamic shared memory, once per kernel (its own `done`) and device.
+bool shared_opt_in(const void *kernel, int bytes, bool *done);
 
 // Keys of a block of consecutive queries [t_first, t_last]: `pad` columns for the first tokens that lie
 // outside the window of the block's first query (n_sink of them real), then one column per token from w0

@@ -319,9 +319,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(DecodeArgs
 template <typename S, bool FP8, int DH>
 hcsa_status launch_simt(const DecodeArgs &a, cudaStream_t st) {
     constexpr int HB = heads_of<DH>(), smem = kWarps * HB * DH * (int)sizeof(float);
-    if (cudaFuncSetAttribute(swa_decode_simt_kernel<S, FP8, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-        cudaSuccess)
-        return HCSA_ERR_CUDA;
+    static bool opted[64];
+    if (!shared_opt_in((const void *)swa_decode_simt_kernel<S, FP8, DH>, smem, opted)) return HCSA_ERR_CUDA;
     const int G = a.H / a.c.Hkv, units = a.c.Hkv * ((G + HB - 1) / HB);
     const bool direct = decode_direct(a);
     if (direct && (int64_t)a.c.B * units > INT32_MAX) return HCSA_ERR_UNSUPPORTED;
@@ -360,6 +359,15 @@ int sm_grid(int per_sm) {
         n[dev] = sms;
     }
     return per_sm * n[dev];
+}
+
+bool shared_opt_in(const void *kernel, int bytes, bool *done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev >= 0 && dev < 64 && done[dev]) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (dev >= 0 && dev < 64) done[dev] = true;
+    return true;
 }
 
 size_t decode_split_bytes(int B, int grid, int heads, int dh) {

@@ -595,8 +595,8 @@ template <int DH, bool FP8, int CT>
 hcsa_status launch(const DecodeArgs &a, cudaStream_t st) {
     using Sh = Shape<DH, FP8, CT>;
     auto kernel = swa_decode_tc_kernel<DH, FP8, CT>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem) != cudaSuccess)
-        return HCSA_ERR_CUDA;
+    static bool opted[64];
+    if (!shared_opt_in((const void *)kernel, Sh::kSmem, opted)) return HCSA_ERR_CUDA;
     CUtensorMap mk, mv;
     const uint64_t rows = (uint64_t)a.c.n_pages * a.c.Hkv * a.c.page;
     const bool made = FP8 ? make_tmap_u8_2d(&mk, a.c.k_pages, DH, rows, DH, DH, CT) &&

@@ -184,9 +184,8 @@ template <typename S, int DH, int BM, int BN>
 hcsa_status launch(const SwaArgs &a, cudaStream_t st) {
     constexpr int smem = (int)sizeof(SimtSmem<S, DH, BM, BN>);
     static_assert(smem <= 232448, "shared memory per CTA");
-    if (cudaFuncSetAttribute(swa_simt_kernel<S, DH, BM, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-        cudaSuccess)
-        return HCSA_ERR_CUDA;
+    static bool opted[64];
+    if (!shared_opt_in((const void *)swa_simt_kernel<S, DH, BM, BN>, smem, opted)) return HCSA_ERR_CUDA;
     const int64_t per = ((int64_t)(a.row1 - a.row0) * (a.H / a.Hkv) + BM - 1) / BM;
     if (per * a.Hkv > INT32_MAX) return HCSA_ERR_UNSUPPORTED;
     swa_simt_kernel<S, DH, BM, BN><<<(unsigned)(per * a.Hkv), 256, smem, st>>>(a, per);

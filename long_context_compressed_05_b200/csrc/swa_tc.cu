@@ -582,8 +582,8 @@ template <int DH>
 hcsa_status launch(const SwaArgs &a, cudaStream_t st) {
     using Sz = Sizes<DH>;
     static_assert(Sz::kSmem <= 232448 && sizeof(Bars<Sz::kStages>) + 16 <= 1024, "shared memory per CTA");
-    if (cudaFuncSetAttribute(swa_tc_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sz::kSmem) != cudaSuccess)
-        return HCSA_ERR_CUDA;
+    static bool opted[64];
+    if (!shared_opt_in((const void *)swa_tc_kernel<DH>, Sz::kSmem, opted)) return HCSA_ERR_CUDA;
     Args p;
     p.a = a;
     p.G = a.H / a.Hkv;
