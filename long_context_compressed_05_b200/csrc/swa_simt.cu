@@ -69,16 +69,39 @@ __global__ void __launch_bounds__(256) swa_simt_kernel(SwaArgs a, int64_t blocks
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
     }
+    // K and V of the next tile wait in registers while this one is worked on
+    constexpr int NL = BN * (DH / V) / 256;
+    static_assert(BN * (DH / V) % 256 == 0, "whole vectors per thread");
+    uint4 kr[NL], vr[NL];
+    auto fetch = [&](int c0) {
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int i = j * 256 + threadIdx.x, c = c0 + i / (DH / V), d = (i % (DH / V)) * V;
+            kr[j] = vr[j] = make_uint4(0, 0, 0, 0);
+            if (c < bk.n && d < a.dh) {
+                const int64_t t = bk.token(c);
+                kr[j] = __ldg(reinterpret_cast<const uint4 *>((const S *)a.k + t * a.ld_k + (int64_t)g * a.dh + d));
+                vr[j] = __ldg(reinterpret_cast<const uint4 *>((const S *)a.v + t * a.ld_v + (int64_t)g * a.dh + d));
+            }
+        }
+    };
+    auto widen = [](const uint4 &raw, float *dst) {
+        const S *e8 = reinterpret_cast<const S *>(&raw);
+#pragma unroll
+        for (int e = 0; e < V; e += 4)
+            *reinterpret_cast<float4 *>(dst + e) =
+                make_float4((float)e8[e], (float)e8[e + 1], (float)e8[e + 2], (float)e8[e + 3]);
+    };
+    fetch(0);
     for (int c0 = 0; c0 < bk.n; c0 += BN) {
         __syncthreads();   // the previous tile's readers are done
-        auto row_of = [&](const void *base, int64_t ld) {
-            return [=](int r) -> const S * {
-                const int c = c0 + r;
-                return c < bk.n ? (const S *)base + (int64_t)bk.token(c) * ld + (int64_t)g * a.dh : nullptr;
-            };
-        };
-        load_rows(sm.k, BN, row_of(a.k, a.ld_k));
-        load_rows(sm.v, BN, row_of(a.v, a.ld_v));
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int i = j * 256 + threadIdx.x, r = i / (DH / V), d = (i % (DH / V)) * V;
+            widen(kr[j], &sm.k[r][d]);
+            widen(vr[j], &sm.v[r][d]);
+        }
+        if (c0 + BN < bk.n) fetch(c0 + BN);
         __syncthreads();
         float s[RM][RN];
 #pragma unroll
