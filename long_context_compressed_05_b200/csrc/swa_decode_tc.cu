@@ -43,7 +43,8 @@ template <int DH, bool FP8, int CT> struct Shape {
     static constexpr int kTile = CT * DH * (FP8 ? 1 : 2);          // K or V of a chunk
     static constexpr int kStage = 2 * kTile;
     static constexpr int kStages = kRingBytes / (kW * kStage) < 8 ? kRingBytes / (kW * kStage) : 8;
-    static constexpr int kSmem = kW * kStages * kStage + 1024;
+    static constexpr int kExps = FP8 ? 2 * CT * (DH / 32) : 0;      // K's exponents, then V's
+    static constexpr int kSmem = kW * kStages * (kStage + kExps) + 1024;
     static_assert(kStages >= 2 && kW * kHB * DH * 4 <= kW * kStages * kStage, "the join fits in the ring");
 };
 
@@ -137,11 +138,12 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
     const int G = a.H / a.c.Hkv, blocks = (G + kHB - 1) / kHB;
     const float scale = a.scale * 1.4426950408889634f;
     if (lane == 0) {
-        for (int i = 0; i < NST; ++i) tc::mbar_init(&bars[warp][i], 1);
+        for (int i = 0; i < NST; ++i) tc::mbar_init(&bars[warp][i], FP8 ? 33 : 1);   // FP8: every lane's exponent copies too
         tc::fence_mbar_init();
     }
     __syncwarp();
     const uint32_t stages = tc::smem_u32(ring) + warp * NST * Sh::kStage;
+    uint8_t *exps = ring + kW * NST * Sh::kStage + warp * NST * Sh::kExps;
     const int64_t exps_at = (int64_t)a.c.n_pages * a.c.Hkv * a.c.page * DH;   // FP8: offset of the exponents
     uint32_t it = 0;                 // chunks this warp has asked for, over all segments
     uint32_t used = 0;               // chunks this warp has consumed
@@ -183,7 +185,7 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
 
         int lines = 0;               // lane i: first row of this warp's chunk (asked & ~31) + i in the page arrays
         int asked = 0;               // of this segment
-        auto ask = [&]() -> uint2 {  // whole warp; returns (FP8) the exponents of K and V row lane % CT
+        auto ask = [&]() {           // whole warp
             if ((asked & 31) == 0 && asked + lane < mine) {
                 const int j0 = dk.token(sg.c0 + warp + (asked + lane) * kW), nth = j0 / a.c.page;
                 int id = a.c.table[(int64_t)sg.b * a.c.max_pages + nth];
@@ -205,22 +207,19 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                     tc::tma_load_2d(dst + Sh::kTile + c * CT * 128, &tm_v, c * 64, line, bar);
                 }
             }
+            if constexpr (FP8) {     // CT rows' exponents, contiguous: 16 bytes a lane, K's then V's
+                constexpr int kVecs = Sh::kExps / 32;
+                if (lane < 2 * kVecs) {
+                    const uint8_t *src = (const uint8_t *)(lane < kVecs ? a.c.k_pages : a.c.v_pages) + exps_at +
+                                         (int64_t)line * NB + (lane % kVecs) * 16;
+                    tc::cp_async16(tc::smem_u32(exps + it % NST * Sh::kExps + lane * 16), src, true);
+                }
+                tc::cp_async_arrive_noinc(&bars[warp][it % NST]);
+            }
             ++it;
             ++asked;
-            if constexpr (FP8) {
-                const int64_t at = exps_at + ((int64_t)line + (lane & (CT - 1))) * NB;
-                const uint8_t *ks = (const uint8_t *)a.c.k_pages + at, *vs = (const uint8_t *)a.c.v_pages + at;
-                if constexpr (NB == 4)
-                    return make_uint2(__ldg(reinterpret_cast<const uint32_t *>(ks)), __ldg(reinterpret_cast<const uint32_t *>(vs)));
-                else   // unused bytes repeat used ones
-                    return make_uint2(__ldg(reinterpret_cast<const uint16_t *>(ks)) * 0x00010001u,
-                                      __ldg(reinterpret_cast<const uint16_t *>(vs)) * 0x00010001u);
-            }
-            return make_uint2(0, 0);
         };
-        uint2 exps[NST];             // FP8: of the next chunks
-#pragma unroll
-        for (int i = 0; i < NST; ++i) exps[i] = i < mine ? ask() : make_uint2(0, 0);
+        for (int i = 0; i < NST && i < mine; ++i) ask();
 
         // Q fragments: 16 heads x 16 channels a step; rows past the group are zero.  FP8: channels 4 cq .. + 3 of the
         // step, as its code words have them
@@ -304,7 +303,16 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
             }
             // FP8: this lane's words of exponents against the references: z = 4 (e - E + 15) by byte, the upper byte of
             // the fp16 number 2^(e - E), where e - E is in [-8, 7]
-            uint2 ew = exps[0], z = ew;
+            uint2 ew = make_uint2(0, 0);
+            if constexpr (FP8) {     // K and V row lane % CT; unused bytes repeat used ones
+                const uint8_t *ex = exps + st * Sh::kExps + (lane & (CT - 1)) * NB;
+                if constexpr (NB == 4)
+                    ew = make_uint2(*reinterpret_cast<const uint32_t *>(ex), *reinterpret_cast<const uint32_t *>(ex + CT * NB));
+                else
+                    ew = make_uint2(*reinterpret_cast<const uint16_t *>(ex) * 0x00010001u,
+                                    *reinterpret_cast<const uint16_t *>(ex + CT * NB) * 0x00010001u);
+            }
+            uint2 z = ew;
             bool k_fast = q16, v_fast = true;
             if constexpr (FP8) {
                 const bool hidden = !whole && !dk.seen(j0 + (lane & (CT - 1)), a.sinks);
@@ -503,9 +511,7 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                 }
             }
             __syncwarp();            // every lane has read the stage
-#pragma unroll
-            for (int x = 0; x + 1 < NST; ++x) exps[x] = exps[x + 1];
-            exps[NST - 1] = asked < mine ? ask() : make_uint2(0, 0);
+            if (asked < mine) ask();
         }
 
         // ------------------------------------------------ join of the warps
