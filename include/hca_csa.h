@@ -154,7 +154,8 @@ typedef struct {
  *                  (bf16 layers, dh a multiple of 32) the FP8 layout of hcsa_params.lowprec over the
  *                  n_pages * Hkv * page rows of dh channels: all codes, then all int8 exponents
  *                  (hcsa_page_bytes gives the size)
- * page_table       [B, max_pages] int32; entries past a sequence's last page are not read */
+ * page_table       [B, max_pages] int32; a decode step reads the entries of pages that hold a token it sees, so pages
+ *                  between the first tokens and the window may be given back (entry -1) */
 typedef struct {
     void *k_pages;
     void *v_pages;
@@ -395,8 +396,8 @@ hcsa_status csa_decode_index_topk_noalloc(const hcsa_params *p, const hcsa_cache
 /* Bytes of one of the two page arrays (n_pages, Hkv, page, dh, dtype, lowprec); 0 for a NULL p. */
 size_t hcsa_page_bytes(const hcsa_params *p);
 
-/* Causal prefill of one sequence of p->T tokens (or its row range p->row0 .. p->row1: such a call reads no
- * key / value row outside [row0 - window + 1, row1) and [0, sinks)).
+/* Causal prefill of one sequence of p->T tokens (or its row range p->row0 .. p->row1: such a call uses no
+ * key / value row outside [row0 - window + 1, row1) and [0, sinks), and reads none behind row1).
  *   q [T, ld_q] (H*dh used, head-major), k [T, ld_k], v [T, ld_v] (Hkv*dh used each), out [T, ld_out] (H*dh
  *   columns written).  A key or value that no query of a row may see never reaches that row, whatever it
  *   holds (infinities and NaN included). */
@@ -429,8 +430,8 @@ hcsa_status swa_decode_attend(const hcsa_params *p, const hcsa_pages *pages, con
  * normalisation; this is the usual one):
  *     s = x + delta,  x_out = round(s),  y = s / sqrt(mean(s^2) + eps) * w
  * with s and the mean in fp32 or wider, each result rounded once.
- *   x [rows, ld_x]; delta [rows, ld_delta] or NULL (s = x); w [D]; x_out [rows, ld_xo] or NULL, may be x itself
- *   y  [rows, ld_y] in p->dtype, or NULL
+ *   x [rows, ld_x]; delta [rows, ld_delta] or NULL (s = x); w [D]; x_out [rows, ld_xo] or NULL, may be x or delta itself
+ *   y  [rows, ld_y] in p->dtype, or NULL; not x_out, and with y8 neither x nor delta
  *   y8 or NULL (bf16 layers, D a multiple of 32): y in the FP8 layout of hcsa_params.lowprec: rows x D
  *      bytes of E4M3 codes, then rows x D/32 int8 exponents, rounded once from y (not from its bf16 value);
  *      each exponent is the one of the exact y even where a block's maximum lies next to a power-of-two

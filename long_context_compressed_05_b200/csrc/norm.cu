@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(NormArgs a, int tpr) 
             if (a.delta) d[i] = *reinterpret_cast<const uint4 *>(dr + c * V);
         }
     }
-    // FP8 with x_out = x: x is stored last, from a second reading, since the exact path reads it again
-    const bool in_place = FP8 && a.x_out == a.x;
+    // FP8 with x_out = x (or delta): stored last, from a second reading, since the exact path reads them again
+    const bool in_place = FP8 && a.x_out && (a.x_out == a.x || a.x_out == a.delta);
     float v[VPT][V], part[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) part[e] = 0.f;

@@ -198,8 +198,10 @@ __global__ void __launch_bounds__(256) swa_simt_kernel(SwaArgs a, int64_t blocks
     for (int r = threadIdx.x >> 5; r < BM; r += 8) {
         if (!sm.bad[r]) continue;
         const int t = (int)((r0 + r) / G);
-        if (values_bad<S>(a, g, bk.w0, (int64_t)t - a.window + 1, lane) || values_bad<S>(a, g, t + 1, t_last + 1, lane))
-            attend_row<S>(a, t, g * G + (int)((r0 + r) % G), lane, 0, a.dh);
+        const int h = g * G + (int)((r0 + r) % G);
+        if ((values_bad<S>(a, g, bk.w0, (int64_t)t - a.window + 1, lane) || values_bad<S>(a, g, t + 1, t_last + 1, lane)) &&
+            !row_explained<S>(a, t, h, lane, 0, a.dh))
+            attend_row<S>(a, t, h, lane, 0, a.dh);
     }
 }
 

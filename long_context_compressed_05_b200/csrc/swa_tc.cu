@@ -564,12 +564,14 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             unf2(zero, z0, z1);
             // rows that are not finite: by a value that they do not see? (the columns loaded for the block)
             for (unsigned bad = __ballot_sync(0xffffffffu, row_ok && z0 + z1 != 0.f); bad; bad &= bad - 1) {
-                const int row = quad * 32 + __ffs(bad) - 1, rt = ta + row / p.G;
+                __syncwarp();        // the row as its thread has stored it
+                const int row = quad * 32 + __ffs(bad) - 1, rt = ta + row / p.G, rh = x.g * p.G + row % p.G;
                 const int behind = min(a.row1, x.w0 + x.c.n_tiles * kKT - x.c.pad);
-                if (values_bad<__nv_bfloat16>(a, x.g, x.w0, (int64_t)rt - a.window + 1, lane) ||
-                    values_bad<__nv_bfloat16>(a, x.g, rt + 1, behind, lane) ||
-                    (x.c.pad && values_bad<__nv_bfloat16>(a, x.g, x.c.sk, x.c.pad, lane)))
-                    attend_row<__nv_bfloat16>(a, rt, x.g * p.G + row % p.G, lane, 0, DH);
+                if ((values_bad<__nv_bfloat16>(a, x.g, x.w0, (int64_t)rt - a.window + 1, lane) ||
+                     values_bad<__nv_bfloat16>(a, x.g, rt + 1, behind, lane) ||
+                     (x.c.pad && values_bad<__nv_bfloat16>(a, x.g, x.c.sk, x.c.pad, lane))) &&
+                    !row_explained<__nv_bfloat16>(a, rt, rh, lane, 0, DH))
+                    attend_row<__nv_bfloat16>(a, rt, rh, lane, 0, DH);
             }
         }
     }

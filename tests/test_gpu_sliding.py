@@ -646,3 +646,63 @@ def test_norm_fp8_in_place(h):
     h.hcsa_add_rmsnorm(p, x, d, w, 1e-6, xo, None, y8[0])
     h.hcsa_add_rmsnorm(p, x, d, w, 1e-6, x, None, y8[1])
     assert torch.equal(x, xo) and torch.equal(y8[0], y8[1])
+
+
+@pytest.mark.parametrize("dtype,dh,window", [("bf16", 128, NO_WINDOW), ("bf16", 64, 200), ("f32", 64, 300), ("bf16", 72, 90)])
+def test_attend_a_bad_channel_leaves_the_others(h, dtype, dh, window):
+    """One channel infinite in every value: that channel is not finite, the others are as without it, and it takes no
+    key-by-key pass over the rows."""
+    T, H, Hkv = 2500, 4, 2
+    g = gen(61)
+    q, k, v = (randn(g, T, n * dh, dtype=dt(dtype)) for n in (H, Hkv, Hkv))
+    v2 = v.clone()
+    v2.view(T, Hkv, dh)[:, :, 5] = math.inf
+    p = attend_params(h, T, H, Hkv, dh, window, 3, dtype)
+    out = torch.empty_like(q)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    h.swa_attend(p, q, k, v2, out)
+    end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) < 500
+    got = out.view(T, H, dh)
+    assert not torch.isfinite(got[:, :, 5].float()).any()
+    mask = seen_mask(torch.arange(T, device="cuda"), T, window, 3)
+    got[:, :, 5] = 0
+    v.view(T, Hkv, dh)[:, :, 5] = 0
+    check(out, q.view(T, H, dh), k.view(T, Hkv, dh), v.view(T, Hkv, dh), mask, p.scale, dtype)
+
+
+@pytest.mark.parametrize("kind,dh", [("bf16", 128), ("fp8", 64), ("f32", 64)])
+def test_decode_pages_behind_the_window_may_be_given_back(h, kind, dh):
+    c = Paged(h, [900, 333], 8, 2, dh, 100, 5, 32, "f32" if kind == "f32" else "bf16", kind == "fp8", seed=71)
+    want = c.decode()
+    for b, x in enumerate(c.pos_h):
+        for i in range(c.table.shape[1]):
+            if 32 * i >= 5 and 32 * i + 31 <= x - 100:       # no token of the page is seen
+                c.table[b, i] = -1
+    assert torch.equal(c.decode(), want)                     # (the status word is checked at the end)
+
+
+def test_calls_on_another_stream_than_the_inputs_and_given_streams(h):
+    """stream=: the call runs there; inputs made on one stream, used on another after a wait."""
+    side = torch.cuda.Stream()
+    g = gen(81)
+    x, d, w = randn(g, 500, 512), randn(g, 500, 512), randn(g, 512)
+    xo, y = torch.empty_like(x), torch.empty_like(x)
+    p = h.make_params(D=512)
+    side.wait_stream(torch.cuda.current_stream())
+    h.hcsa_add_rmsnorm(p, x, d, w, 1e-6, xo, y, stream=side)
+    side.synchronize()
+    xo2, y2 = torch.empty_like(x), torch.empty_like(x)
+    h.hcsa_add_rmsnorm(p, x, d, w, 1e-6, xo2, y2)
+    assert torch.equal(xo, xo2) and torch.equal(y, y2)
+
+
+def test_cpu_tensors_are_refused(h):
+    x, w = torch.zeros(3, 64, dtype=torch.bfloat16), torch.ones(64, dtype=torch.bfloat16)
+    p = h.make_params(D=64)
+    for args in ((x, None, w, 1e-6, None, x.clone()), (x.cuda(), None, w, 1e-6, None, x.cuda())):
+        with pytest.raises(h.HcsaError) as e:
+            h.hcsa_add_rmsnorm(p, *args)
+        assert e.value.code == 2

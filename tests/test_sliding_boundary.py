@@ -161,3 +161,11 @@ def test_python_wrappers_check_what_the_library_cannot_see(h):
         with pytest.raises(h.HcsaError) as e:
             call()
         assert e.value.code == code
+
+
+def test_norm_refuses_outputs_over_what_it_reads_again(h):
+    p = h.make_params(D=256)
+    other = 0x20000
+    assert norm(h, p, xo=other, y=other) == 8
+    assert norm(h, p, delta=0x30000, xo=0, y=FAKE, y8=0x40000) == 8          # y over x
+    assert norm(h, p, delta=other, xo=0, y=other, y8=0x40000) == 8           # y over delta
