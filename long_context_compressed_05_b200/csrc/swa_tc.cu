@@ -4,18 +4,23 @@
 // A block is two sub-tiles of 128 query rows of one key head: a row is a (token, head of the group) pair, a sub-tile
 // holds floor(128 / G) tokens.  Both sub-tiles walk the same tiles of 128 key columns (the first tokens outside the
 // window, padded to 16, then the tokens from the first row's window on; see block_keys) and share their loads.
-//   S = Q K^T        steps of 64 columns, 128 x 64 fp32 in TMEM, two buffers per sub-tile: S of the next step is ready
-//                    when a step's softmax ends (with one buffer of 128 columns, which P then needs, products and
-//                    softmax of a sub-tile ran one after the other: 466 us against XX at 8192 tokens, 32 heads)
+//   S = Q K^T        128 x 128 fp32 in TMEM, one buffer per sub-tile
 //   online softmax   a warpgroup per sub-tile, a thread per row (no exchange between threads); the running maximum is
 //                    raised, and O rescaled in TMEM, only when a row's maximum grows by more than 2^8
-//   O += P V         P (bf16) as the A operand in TMEM, written over S; V an MN-major B operand from shared memory
-// Each sub-tile has its own issuing warp; the S of the next block is issued while the last steps of this one run.
-// Persistent CTAs take the blocks longest first, in a snake order over the CTAs.  Warps: 0 and 3 TMA, 1 and 2 MMA, 4..7 and
-// 8..11 softmax and output of sub-tile 0 and 1.
+//   O += P V         P (bf16) as the A operand in TMEM, written over S and handed over in two parts (96 + 32 columns), so
+//                    that only the last 32 keys' products are left when the softmax ends; V an MN-major B operand
+// Each sub-tile has its own issuing warp.  They take turns, and a turn issues the end of a P V and the next S behind it
+// (also across blocks), so that one sub-tile's products run while the other's softmax does.  Persistent CTAs take the
+// blocks longest first, in a snake order over the CTAs.  Warps: 0 and 3 TMA, 1 and 2 MMA, 4..7 and 8..11 softmax and
+// output of sub-tile 0 and 1.
 //
 // Per tile of 128 x 128 at dh 128 the products take 1024 cycles of the tensor core and the exponentials 1024 of
-// the special-function unit: two equal bounds for a long window.
+// the special-function unit: two equal bounds for a long window.  What holds it above them is the chain of a
+// sub-tile (S, softmax, P V, next S), of which TMEM has room for two.  Measured at 8192 tokens, 32 heads over 8, dh 128,
+// causal: 409 us (1345 TFLOP/s).  What was tried there: P in one part 462; parts of 64 + 64 462, four of 32 479; two
+// threads per row 466; two S buffers of 64 columns 458 (the narrow products are bound by shared memory); a quarter of
+// the exponentials by a polynomial on the FMA pipe 441; one issuing warp for both sub-tiles 497.  A window of 128 (65536
+// tokens, 64 heads over 8, dh 128: 680 us) is bound by the same chain: two tiles a block, then the output.
 #include "sliding.cuh"
 #include "tc_common.cuh"
 
