@@ -2,38 +2,57 @@
 // not take.  Flash-style: a block owns BM consecutive (token, head of the group) rows of one key head and walks
 // the keys its tokens see in tiles of BN, all operands in shared memory as fp32, online softmax.
 //
-// 256 threads as 16 x 16: thread (ty, tx) owns rows ty RM .. and key columns tx + 16 j of a score tile, and
-// dims 4 tx + 64 j of the output rows.  Bound by the FP32 pipe and shared-memory reads (each 16-byte read feeds
-// eight FMAs at BM = 64, BN = 32).
+// A group of 128 threads as 16 x 8: thread (ty, tx) owns rows ty + 16 i, key columns tx + 8 j of a score tile, and dims
+// 4 tx + 32 j of the output rows.  A warp is then 4 rows x 8 columns, whose 16-byte reads touch each bank once, and RM =
+// RN = 4 make 64 FMAs of eight reads.  Up to dh 64 a block has two groups, which take every other tile of keys and are
+// joined at the end: a short window over a few thousand tokens has too few blocks to hide the reads' latency otherwise
+// (2048 tokens, 8 heads of 64, window 128: 45.4 us, 48.8 with one group).  Bound by issue of FMAs between reads (4096 tokens, 16 heads
+// of 128, window 1000: 932 us, 42% of the FP32 rate; 1143 as 256 threads of 16 x 16 with 32 FMAs of six reads).
 #include "sliding.cuh"
 
 namespace hcsa {
 
 namespace {
 
+constexpr int kThreads = 128;       // of a group
+template <int DH> constexpr int groups_of() { return DH <= 64 ? 2 : 1; }
+
 template <typename S, int DH, int BM, int BN>
 struct SimtSmem {
-    float q[BM][DH + 4], k[BN][DH + 4], v[BN][DH], p[BM][BN + 4];
+    struct Tile {
+        float k[BN][DH + 4], v[BN][DH], p[BM][BN + 4];
+    };
+    float q[BM][DH + 4];
+    Tile t[groups_of<DH>()];
     int bad[BM];
 };
 
 template <typename S, int DH, int BM, int BN>
-__global__ void __launch_bounds__(256) swa_simt_kernel(SwaArgs a, int64_t blocks_per_head) {
-    constexpr int V = Traits<S>::VEC, RM = BM / 16, RN = BN / 16, DN = DH / 64;
+__global__ void __launch_bounds__(kThreads * groups_of<DH>(), DH <= 64 ? 2 : DH <= 128 ? 3 : 1) swa_simt_kernel(SwaArgs a, int64_t blocks_per_head) {
+    constexpr int V = Traits<S>::VEC, RM = BM / 16, RN = BN / 8, DN = DH / 32;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     SimtSmem<S, DH, BM, BN> &sm = *reinterpret_cast<SimtSmem<S, DH, BM, BN> *>(smem_raw);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    constexpr int NG = groups_of<DH>();
+    const int tid = threadIdx.x % kThreads, group = threadIdx.x / kThreads;
+    typename SimtSmem<S, DH, BM, BN>::Tile &tile = sm.t[group];
+    const int tx = tid & 7, ty = tid >> 3;
+    auto sync_group = [&]() {
+        if (NG == 1) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kThreads) : "memory");
+    };
     const int G = a.H / a.Hkv;
     const int g = (int)(blockIdx.x / blocks_per_head);
     // latest tokens (the most keys) first
     const int64_t r0 = (int64_t)a.row0 * G + (blocks_per_head - 1 - blockIdx.x % blocks_per_head) * BM;
     const int64_t r_end = (int64_t)a.row1 * G;
     const int64_t r_last = (r0 + BM < r_end ? r0 + BM : r_end) - 1;
-    const BlockKeys bk = block_keys((int)(r0 / G), (int)(r_last / G), a.window, a.sinks, 1);
+    // row r of the block: token t_first + (rem + r) / G, head (rem + r) % G of the group
+    const int t_first = (int)(r0 / G), t_end = (int)(r_last / G), rem = (int)(r0 % G), n_rows = (int)(r_last - r0) + 1;
+    const BlockKeys bk = block_keys(t_first, t_end, a.window, a.sinks, 1);
     const float scale = a.scale * 1.4426950408889634f;
 
     auto load_rows = [&](auto &dst, int rows, auto src_of) {   // src_of(row): pointer or nullptr (zeros)
-        for (int i = threadIdx.x; i < rows * (DH / V); i += 256) {
+        for (int i = threadIdx.x; i < rows * (DH / V); i += kThreads * NG) {
             const int r = i / (DH / V), c = (i % (DH / V)) * V;
             const S *src = src_of(r);
             float f[V];
@@ -51,9 +70,9 @@ __global__ void __launch_bounds__(256) swa_simt_kernel(SwaArgs a, int64_t blocks
         }
     };
     load_rows(sm.q, BM, [&](int r) -> const S * {
-        const int64_t row = r0 + r;
-        if (row > r_last) return nullptr;
-        return (const S *)a.q + (row / G) * a.ld_q + (int64_t)(g * G + (int)(row % G)) * a.dh;
+        if (r >= n_rows) return nullptr;
+        const int x = rem + r, t = x / G;
+        return (const S *)a.q + (int64_t)(t_first + t) * a.ld_q + (int64_t)(g * G + x - t * G) * a.dh;
     });
 
     float o[RM][DN][4], m[RM], l[RM];
@@ -62,21 +81,22 @@ __global__ void __launch_bounds__(256) swa_simt_kernel(SwaArgs a, int64_t blocks
     for (int i = 0; i < RM; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
-        const int64_t row = r0 + ty * RM + i;
-        tok[i] = row <= r_last ? (int)(row / G) : -1;
+        const int r = ty + 16 * i;
+        tok[i] = r < n_rows ? t_first + (rem + r) / G : -1;
 #pragma unroll
         for (int j = 0; j < DN; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
     }
     // K and V of the next tile wait in registers while this one is worked on
-    constexpr int NL = BN * (DH / V) / 256;
-    static_assert(BN * (DH / V) % 256 == 0, "whole vectors per thread");
+    constexpr int NL = BN * (DH / V) / kThreads;
+    static_assert(BN * (DH / V) % kThreads == 0, "whole vectors per thread");
+    constexpr bool kAhead = NL <= 4;   // else there are no registers for it
     uint4 kr[NL], vr[NL];
     auto fetch = [&](int c0) {
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
-            const int i = j * 256 + threadIdx.x, c = c0 + i / (DH / V), d = (i % (DH / V)) * V;
+            const int i = j * kThreads + tid, c = c0 + i / (DH / V), d = (i % (DH / V)) * V;
             kr[j] = vr[j] = make_uint4(0, 0, 0, 0);
             if (c < bk.n && d < a.dh) {
                 const int64_t t = bk.token(c);
@@ -92,30 +112,34 @@ __global__ void __launch_bounds__(256) swa_simt_kernel(SwaArgs a, int64_t blocks
             *reinterpret_cast<float4 *>(dst + e) =
                 make_float4((float)e8[e], (float)e8[e + 1], (float)e8[e + 2], (float)e8[e + 3]);
     };
-    fetch(0);
-    for (int c0 = 0; c0 < bk.n; c0 += BN) {
-        __syncthreads();   // the previous tile's readers are done
+    if (kAhead) fetch(group * BN);
+    __syncthreads();       // Q
+    for (int c0 = group * BN; c0 < bk.n; c0 += NG * BN) {
+        sync_group();      // the previous tile's readers are done
+        if (!kAhead) fetch(c0);
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
-            const int i = j * 256 + threadIdx.x, r = i / (DH / V), d = (i % (DH / V)) * V;
-            widen(kr[j], &sm.k[r][d]);
-            widen(vr[j], &sm.v[r][d]);
+            const int i = j * kThreads + tid, r = i / (DH / V), d = (i % (DH / V)) * V;
+            widen(kr[j], &tile.k[r][d]);
+            widen(vr[j], &tile.v[r][d]);
         }
-        if (c0 + BN < bk.n) fetch(c0 + BN);
-        __syncthreads();
+        if (kAhead && c0 + NG * BN < bk.n) fetch(c0 + NG * BN);
+        sync_group();
+        // every column seen by every row?
+        const bool clean = c0 >= bk.pad && bk.token(c0 + BN - 1) <= t_first && bk.token(c0) > t_end - a.window;
         float s[RM][RN];
 #pragma unroll
         for (int i = 0; i < RM; ++i)
 #pragma unroll
             for (int j = 0; j < RN; ++j) s[i][j] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
         for (int d = 0; d < DH; d += 4) {
             float4 kq[RN];
 #pragma unroll
-            for (int j = 0; j < RN; ++j) kq[j] = *reinterpret_cast<const float4 *>(&sm.k[tx + 16 * j][d]);
+            for (int j = 0; j < RN; ++j) kq[j] = *reinterpret_cast<const float4 *>(&tile.k[tx + 8 * j][d]);
 #pragma unroll
             for (int i = 0; i < RM; ++i) {
-                const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[ty * RM + i][d]);
+                const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[ty + 16 * i][d]);
 #pragma unroll
                 for (int j = 0; j < RN; ++j)
                     s[i][j] += qv.x * kq[j].x + qv.y * kq[j].y + qv.z * kq[j].z + qv.w * kq[j].w;
@@ -126,13 +150,13 @@ __global__ void __launch_bounds__(256) swa_simt_kernel(SwaArgs a, int64_t blocks
             float mt = m[i];
 #pragma unroll
             for (int j = 0; j < RN; ++j) {
-                const int c = c0 + tx + 16 * j;
-                const bool seen = c < bk.n && column_seen(bk, c, tok[i], a.window, a.sinks);
+                const int c = c0 + tx + 8 * j;
+                const bool seen = clean || (c < bk.n && column_seen(bk, c, tok[i], a.window, a.sinks));
                 s[i][j] = seen ? s[i][j] * scale : -INFINITY;
                 mt = fmaxf(mt, s[i][j]);
             }
 #pragma unroll
-            for (int q = 8; q; q >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, q));
+            for (int q = 4; q; q >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, q));
             const float ref = mt == -INFINITY ? 0.f : mt;   // a row that has seen no key yet: every weight 0
             const float f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - ref);
             m[i] = mt;
@@ -141,7 +165,7 @@ __global__ void __launch_bounds__(256) swa_simt_kernel(SwaArgs a, int64_t blocks
             for (int j = 0; j < RN; ++j) {
                 const float p = exp2f(s[i][j] - ref);
                 sum += p;
-                sm.p[ty * RM + i][tx + 16 * j] = p;
+                tile.p[ty + 16 * i][tx + 8 * j] = p;
             }
             l[i] = l[i] * f + sum;
 #pragma unroll
@@ -149,17 +173,17 @@ __global__ void __launch_bounds__(256) swa_simt_kernel(SwaArgs a, int64_t blocks
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][j][e] *= f;
         }
-        __syncwarp();   // a row's 16 threads are in one warp
+        __syncwarp();   // a row's 8 threads are in one warp
 #pragma unroll 2
         for (int c = 0; c < BN; c += 4) {
             float4 p[RM];
 #pragma unroll
-            for (int i = 0; i < RM; ++i) p[i] = *reinterpret_cast<const float4 *>(&sm.p[ty * RM + i][c]);
+            for (int i = 0; i < RM; ++i) p[i] = *reinterpret_cast<const float4 *>(&tile.p[ty + 16 * i][c]);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int j = 0; j < DN; ++j) {
-                    const float4 vv = *reinterpret_cast<const float4 *>(&sm.v[c + e][4 * tx + 64 * j]);
+                    const float4 vv = *reinterpret_cast<const float4 *>(&tile.v[c + e][4 * tx + 32 * j]);
 #pragma unroll
                     for (int i = 0; i < RM; ++i) {
                         const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
@@ -172,18 +196,46 @@ __global__ void __launch_bounds__(256) swa_simt_kernel(SwaArgs a, int64_t blocks
         }
     }
     if (threadIdx.x < BM) sm.bad[threadIdx.x] = 0;
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int q = 4; q; q >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], q);
     __syncthreads();
+    if constexpr (NG == 2) {   // the second group's rows through its tile's memory
+        float *x = reinterpret_cast<float *>(&sm.t[1]) + tid;
+        constexpr int kEach = 2 + 4 * DN;
+        static_assert(RM * kEach * kThreads * sizeof(float) <= sizeof(sm.t[1]), "the join fits");
+        if (group == 1) {
+#pragma unroll
+            for (int i = 0; i < RM; ++i) {
+                x[(i * kEach) * kThreads] = m[i];
+                x[(i * kEach + 1) * kThreads] = l[i];
+#pragma unroll
+                for (int j = 0; j < 4 * DN; ++j) x[(i * kEach + 2 + j) * kThreads] = o[i][j / 4][j % 4];
+            }
+        }
+        __syncthreads();
+        if (group == 0) {
+#pragma unroll
+            for (int i = 0; i < RM; ++i) {
+                const float m1 = x[(i * kEach) * kThreads], l1 = x[(i * kEach + 1) * kThreads], mm = fmaxf(m[i], m1);
+                const float ref = mm == -INFINITY ? 0.f : mm;
+                const float f0 = m[i] == -INFINITY ? 0.f : exp2f(m[i] - ref), f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - ref);
+                l[i] = l[i] * f0 + l1 * f1;
+#pragma unroll
+                for (int j = 0; j < 4 * DN; ++j)
+                    o[i][j / 4][j % 4] = o[i][j / 4][j % 4] * f0 + x[(i * kEach + 2 + j) * kThreads] * f1;
+            }
+        }
+    }
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
-#pragma unroll
-        for (int q = 8; q; q >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], q);
-        if (tok[i] < 0) continue;
-        const int64_t row = r0 + ty * RM + i;
-        S *dst = (S *)a.out + (int64_t)tok[i] * a.ld_out + (int64_t)(g * G + (int)(row % G)) * a.dh;
+        if (tok[i] < 0 || group) continue;
+        S *dst = (S *)a.out + (int64_t)tok[i] * a.ld_out + (int64_t)(g * G + (rem + ty + 16 * i) % G) * a.dh;
         bool fine = true;
 #pragma unroll
         for (int j = 0; j < DN; ++j) {
-            const int d = 4 * tx + 64 * j;
+            const int d = 4 * tx + 32 * j;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float y = o[i][j][e] / l[i];
@@ -191,15 +243,14 @@ __global__ void __launch_bounds__(256) swa_simt_kernel(SwaArgs a, int64_t blocks
                 if (d + e < a.dh) store_val(dst + d + e, y);
             }
         }
-        if (!fine) sm.bad[ty * RM + i] = 1;
+        if (!fine) sm.bad[ty + 16 * i] = 1;
     }
     __syncthreads();
-    const int t_last = (int)(r_last / G), lane = threadIdx.x & 31;
-    for (int r = threadIdx.x >> 5; r < BM; r += 8) {
+    const int lane = threadIdx.x & 31;
+    for (int r = threadIdx.x >> 5; r < BM; r += kThreads * NG / 32) {
         if (!sm.bad[r]) continue;
-        const int t = (int)((r0 + r) / G);
-        const int h = g * G + (int)((r0 + r) % G);
-        if ((values_bad<S>(a, g, bk.w0, (int64_t)t - a.window + 1, lane) || values_bad<S>(a, g, t + 1, t_last + 1, lane)) &&
+        const int t = t_first + (rem + r) / G, h = g * G + (rem + r) % G;
+        if ((values_bad<S>(a, g, bk.w0, (int64_t)t - a.window + 1, lane) || values_bad<S>(a, g, t + 1, t_end + 1, lane)) &&
             !row_explained<S>(a, t, h, lane, 0, a.dh))
             attend_row<S>(a, t, h, lane, 0, a.dh);
     }
@@ -213,7 +264,7 @@ hcsa_status launch(const SwaArgs &a, cudaStream_t st) {
     if (!shared_opt_in((const void *)swa_simt_kernel<S, DH, BM, BN>, smem, opted)) return HCSA_ERR_CUDA;
     const int64_t per = ((int64_t)(a.row1 - a.row0) * (a.H / a.Hkv) + BM - 1) / BM;
     if (per * a.Hkv > INT32_MAX) return HCSA_ERR_UNSUPPORTED;
-    swa_simt_kernel<S, DH, BM, BN><<<(unsigned)(per * a.Hkv), 256, smem, st>>>(a, per);
+    swa_simt_kernel<S, DH, BM, BN><<<(unsigned)(per * a.Hkv), kThreads * groups_of<DH>(), smem, st>>>(a, per);
     count_launch();
     return check_launch();
 }
