@@ -706,3 +706,24 @@ def test_cpu_tensors_are_refused(h):
         with pytest.raises(h.HcsaError) as e:
             h.hcsa_add_rmsnorm(p, *args)
         assert e.value.code == 2
+
+
+@pytest.mark.parametrize("dtype,H,Hkv,dh", [("bf16", 64, 8, 128), ("f32", 64, 2, 64)])
+def test_attend_offsets_past_32_bits(h, dtype, H, Hkv, dh):
+    """Queries and outputs of more than 2^31 elements: the last rows, and some in the middle."""
+    T, window, sinks = 2 ** 31 // (H * dh) + 3000, 60, 3
+    g = gen(91)
+    q = torch.empty(T, H * dh, dtype=dt(dtype), device="cuda").normal_(generator=g)
+    k, v = (torch.empty(T, Hkv * dh, dtype=dt(dtype), device="cuda").normal_(generator=g) for _ in range(2))
+    out = torch.empty_like(q)
+    h.swa_attend(attend_params(h, T, H, Hkv, dh, window, sinks, dtype), q, k, v, out)
+    for a in (0, T // 2, T - 40):
+        lo = max(0, a - window)
+        rows = torch.arange(a, a + 40, device="cuda")
+        cols = torch.cat([torch.arange(min(sinks, lo), device="cuda"), torch.arange(lo, a + 40, device="cuda")])
+        t, j = rows[:, None], cols[None]
+        mask = (j <= t) & ((j > t - window) | (j < sinks))
+        check(out[a:a + 40], q[a:a + 40].view(40, H, dh), k[cols].view(-1, Hkv, dh), v[cols].view(-1, Hkv, dh), mask,
+              dh ** -0.5, dtype)
+    del q, k, v, out
+    torch.cuda.empty_cache()
