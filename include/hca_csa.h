@@ -391,7 +391,8 @@ hcsa_status csa_decode_index_topk_noalloc(const hcsa_params *p, const hcsa_cache
  * Storage: HCSA_BF16 or HCSA_F32.  Products, softmax statistics and sums are fp32 for both types (unlike
  * the other fp32-storage calls, which compute in fp64): the result is rounded once when stored; the
  * tensor-core paths also round each softmax weight to bf16 for the value product.
- * H / Hkv <= 128 and dh <= 512; other shapes return HCSA_ERR_UNSUPPORTED. */
+ * H / Hkv <= 128 and dh <= 512; other shapes return HCSA_ERR_UNSUPPORTED.  Calls of no rows (T = 0, rows = 0) do
+ * nothing, whatever the tensors' addresses. */
 
 /* Bytes of one of the two page arrays (n_pages, Hkv, page, dh, dtype, lowprec); 0 for a NULL p. */
 size_t hcsa_page_bytes(const hcsa_params *p);

@@ -569,8 +569,9 @@ hcsa_status swa_attend(const hcsa_params *p, const void *q, int64_t ld_q, const 
                        int64_t ld_v, void *out, int64_t ld_out, void *stream) {
     HCSA_TRY(check_swa(p));
     if (p->lowprec) return HCSA_ERR_UNSUPPORTED;
-    if (!q || !k || !v || !out) return HCSA_ERR_NULL;
     if (p->T < 0) return HCSA_ERR_SHAPE;
+    if (p->T == 0) return HCSA_OK;   // tensors of no rows may have no address
+    if (!q || !k || !v || !out) return HCSA_ERR_NULL;
     if (!aligned(q) || !aligned(k) || !aligned(v) || !aligned(out)) return HCSA_ERR_ALIGN;
     const int64_t n = (int64_t)p->H * p->dh, nkv = (int64_t)p->Hkv * p->dh;
     if (!ld_ok(p->dtype, ld_q, n) || !ld_ok(p->dtype, ld_k, nkv) || !ld_ok(p->dtype, ld_v, nkv) ||
@@ -588,8 +589,9 @@ hcsa_status swa_page_append(const hcsa_params *p, const hcsa_pages *pages, int64
                             const int32_t *seq, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
                             void *stream) {
     HCSA_TRY(check_pages(p, pages));
-    if (!pos || !k || !v) return HCSA_ERR_NULL;
     if (rows < 0 || (!seq && rows > p->B)) return HCSA_ERR_SHAPE;
+    if (rows == 0) return HCSA_OK;
+    if (!pos || !k || !v) return HCSA_ERR_NULL;
     if (!aligned(k) || !aligned(v) || ((uintptr_t)pos & 3u) || ((uintptr_t)seq & 3u)) return HCSA_ERR_ALIGN;
     const int64_t nkv = (int64_t)p->Hkv * p->dh;
     if (!ld_ok(p->dtype, ld_k, nkv) || !ld_ok(p->dtype, ld_v, nkv)) return HCSA_ERR_ALIGN;
@@ -613,8 +615,8 @@ hcsa_status hcsa_add_rmsnorm(const hcsa_params *p, int64_t rows, const void *x, 
                              int64_t ld_y, void *y8, void *stream) {
     if (!p) return HCSA_ERR_NULL;
     if (p->dtype != HCSA_F32 && p->dtype != HCSA_BF16) return HCSA_ERR_DTYPE;
-    if (!x || !w || (!y && !y8)) return HCSA_ERR_NULL;
     if (rows < 0 || p->D < 1 || !(eps >= 0.f)) return HCSA_ERR_SHAPE;
+    if (rows && (!x || !w || (!y && !y8))) return HCSA_ERR_NULL;
     if (y8 && (p->dtype != HCSA_BF16 || p->D % 32 != 0)) return HCSA_ERR_UNSUPPORTED;
     if (p->D > 16384 || rows > INT32_MAX) return HCSA_ERR_UNSUPPORTED;
     if (!aligned(x) || !aligned(delta) || !aligned(w) || !aligned(x_out) || !aligned(y) || !aligned(y8) ||

@@ -727,3 +727,17 @@ def test_attend_offsets_past_32_bits(h, dtype, H, Hkv, dh):
               dh ** -0.5, dtype)
     del q, k, v, out
     torch.cuda.empty_cache()
+
+
+def test_empty_batches(h):
+    """Tensors of no rows: nothing happens, no error."""
+    x = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    h.hcsa_add_rmsnorm(h.make_params(D=256), x, x.clone(), w, 1e-6, x.clone(), x.clone())
+    p = attend_params(h, 0, 4, 1, 64, 10, 0, "bf16")
+    kv = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    h.swa_attend(p, x, kv, kv, x.clone())
+    c = Paged(h, [5], 4, 1, 64, 10, 0, 16, "bf16")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    h.swa_page_append(c.p, c.pages, none, kv, kv, none)
+    c.check(c.decode())

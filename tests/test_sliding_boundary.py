@@ -169,3 +169,9 @@ def test_norm_refuses_outputs_over_what_it_reads_again(h):
     assert norm(h, p, xo=other, y=other) == 8
     assert norm(h, p, delta=0x30000, xo=0, y=FAKE, y8=0x40000) == 8          # y over x
     assert norm(h, p, delta=other, xo=0, y=other, y8=0x40000) == 8           # y over delta
+
+
+def test_calls_of_no_rows_take_tensors_without_an_address(h):
+    assert attend(h, params(h, T=0), q=0, k=0, v=0, out=0) == 0
+    assert append(h, params(h), pages(h), rows=0, pos=0, k=0, v=0) == 0
+    assert norm(h, h.make_params(D=256), rows=0, x=0, delta=0, xo=0, y=0) == 0
