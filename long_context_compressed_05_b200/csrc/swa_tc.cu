@@ -20,7 +20,8 @@
 // causal: 409 us (1345 TFLOP/s).  What was tried there: P in one part 462; parts of 64 + 64 462, four of 32 479; two
 // threads per row 466; two S buffers of 64 columns 458 (the narrow products are bound by shared memory); a quarter of
 // the exponentials by a polynomial on the FMA pipe 441; one issuing warp for both sub-tiles 497.  A window of 128 (65536
-// tokens, 64 heads over 8, dh 128: 680 us) is bound by the same chain: two tiles a block, then the output.
+// tokens, 64 heads over 8, dh 128: 680 us) is bound by the same chain: two tiles a block, then the output.  These are at
+// 1965 MHz; seconds of such calls run at the power limit, 1500 to 1660 MHz (480 and 820 us).
 #include "sliding.cuh"
 #include "tc_common.cuh"
 
