@@ -21,7 +21,9 @@
 // a chunk whose exponents spread further takes the slow path: bf16 operands by full conversions.  Queries are scaled
 // per head to fp16 by a power of two where that is exact (a ratio of 2^32 between the largest and the smallest
 // channel), else the segment takes the slow path.  Weights are held times 2^11, so their rounding to fp16 is
-// relative (2^-11) down to 2^-25 of the largest.  Codes 2i and 2i + 1 of a word share a register (K), or two keys'
+// relative (2^-11) down to 2^-25 of the largest.  An infinite value is stored as 448 x 2^120 (drop_infinite): it is taken
+// out of the product and its channel set at the end, since O is relative to the V reference and would come out finite.
+// Codes 2i and 2i + 1 of a word share a register (K), or two keys'
 // codes of one channel (V), so channels run in a permuted order that the Q fragments and the stores follow.
 #include "decode_split.cuh"
 #include "tc_common.cuh"
@@ -123,6 +125,51 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int g) {
     }
 }
 
+// FP8 values that no fp32 number holds (448 x 2^120 stands for infinity; NaN codes beside them) out of a chunk's V tile:
+// their codes become zero, and cls, a bit per channel, takes their sign (positive ones first, then negative ones; NaN:
+// both).  Every head gives every seen key a weight, so the class of a channel is the same for all.  Returns the row's
+// exponents, the lowest one for a block without a code left, so that it does not raise the reference.  Out of line: it
+// runs for chunks that hold an exponent of 120 or more.
+template <int DH, int CT>
+__device__ __noinline__ uint32_t drop_infinite(uint8_t *v, uint32_t exps, bool hidden, uint32_t *cls) {
+    constexpr int NB = DH / 32;
+    const int lane = threadIdx.x & 31, row = lane & (CT - 1);
+    for (int b = 0; b < NB; ++b) {
+        uint32_t pos = 0, neg = 0;
+        const int e = (int8_t)(exps >> (8 * b));
+        if (lane < CT && !hidden && e >= 120) {
+            uint32_t left = 0;
+            for (int w = 0; w < 8; ++w) {
+                uint32_t *at = reinterpret_cast<uint32_t *>(v + tile_offset<DH, true, CT>(row, 2 * b + w / 4) + 4 * (w % 4));
+                uint32_t codes = *at;
+                for (int i = 0; i < 4; ++i) {
+                    __nv_fp8_e4m3 c;
+                    c.__x = (uint8_t)(codes >> (8 * i));
+                    const float x = (float)c * lp::pow2f(e);
+                    if (fabsf(x) < INFINITY) continue;
+                    codes &= ~(0xFFu << (8 * i));
+                    if (!(x < 0.f)) pos |= 1u << (4 * w + i);
+                    if (!(x > 0.f)) neg |= 1u << (4 * w + i);
+                }
+                *at = codes;
+                left |= codes & 0x7F7F7F7Fu;   // a negative value far below the scale is -0
+            }
+            if (!left) {
+                for (int i = b; i < 4; i += NB)   // two blocks: their bytes come twice
+                    exps = (exps & ~(0xFFu << (8 * i))) | (uint32_t)(uint8_t)-126 << (8 * i);
+            }
+        }
+        pos = __reduce_or_sync(0xffffffffu, pos);
+        neg = __reduce_or_sync(0xffffffffu, neg);
+        if (lane == 0) {
+            cls[b] |= pos;
+            cls[NB + b] |= neg;
+        }
+    }
+    tc::fence_async_smem();          // ordered before the next TMA write of this stage
+    return __shfl_sync(0xffffffffu, exps, row);
+}
+
 template <int DH, bool FP8, int CT>
 __global__ void __launch_bounds__(32 * kW, kPerSM)
 swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap tm_k,
@@ -133,6 +180,7 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
     __shared__ uint64_t bars[kW][NST];
     __shared__ float sm_m[kW][kHB], sm_l[kW][kHB];
     __shared__ int64_t sh[kW];
+    __shared__ uint32_t sm_cls[kW][2 * NB];   // FP8: channels with an infinite value (positive, negative)
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gr = lane >> 2, cq = lane & 3;
     const int G = a.H / a.c.Hkv, blocks = (G + kHB - 1) / kHB;
@@ -182,6 +230,7 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
         const int g = sg.u / blocks, h0 = (sg.u % blocks) * kHB;
         const int heads = G - h0 < kHB ? G - h0 : kHB;
         const int mine = sg.c1 - sg.c0 > warp ? (sg.c1 - sg.c0 - warp + kW - 1) / kW : 0;   // chunks of this warp
+        if (FP8 && lane < 2 * NB) sm_cls[warp][lane] = 0;
 
         int lines = 0;               // lane i: first row of this warp's chunk (asked & ~31) + i in the page arrays
         int asked = 0;               // of this segment
@@ -327,7 +376,11 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                     if (abs(top) < 60) Ek = top;
                     k_fast = offset(ew.x, Ek, z.x);
                 }
-                if (Ev == -128 || !offset(ew.y, Ev, z.y)) {
+                if (Ev == -128 || Ev > 112 || !offset(ew.y, Ev, z.y)) {   // an exponent of 120 comes here
+                    if (__any_sync(0xffffffffu, !hidden && max4s(ew.y) >= 120)) {
+                        __syncwarp();
+                        ew.y = drop_infinite<DH, CT>(ring + (warp * NST + st) * Sh::kStage + Sh::kTile, ew.y, hidden, sm_cls[warp]);
+                    }
                     const int top = largest(ew.y);
                     if (top > Ev) {
                         const float f = pow2_or_0(Ev - top);   // no value yet: O is zero
@@ -553,6 +606,15 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
                         make_float2(o[2 * j + 1][2 * half], o[2 * j + 1][2 * half + 1]);
                 }
             }
+        }
+        if constexpr (FP8) {
+            __syncwarp();
+            if (__any_sync(0xffffffffu, lane < 2 * NB && sm_cls[warp][lane % (2 * NB)]))
+                for (int b = 0; b < NB; ++b) {
+                    const bool pos = sm_cls[warp][b] >> lane & 1, neg = sm_cls[warp][NB + b] >> lane & 1;
+                    for (int h = 0; (pos || neg) && h < kHB; ++h)
+                        acc[(warp * kHB + h) * DH + 32 * b + lane] = pos && neg ? NAN : pos ? INFINITY : -INFINITY;
+                }
         }
         __syncthreads();
         const bool whole_unit = sg.c1 - sg.c0 == sg.n;

@@ -741,3 +741,50 @@ def test_empty_batches(h):
     none = torch.empty(0, dtype=torch.int32, device="cuda")
     h.swa_page_append(c.p, c.pages, none, kv, kv, none)
     c.check(c.decode())
+
+
+def class_of(x):
+    """0 finite, 1 / -1 infinite, 2 NaN."""
+    return torch.where(torch.isnan(x), 2.0, torch.where(torch.isinf(x), x.sign().double(), 0.0))
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -14])
+@pytest.mark.parametrize("dh", [64, 96, 128])
+@pytest.mark.parametrize("pos,window,page", [([700, 130], NO_WINDOW, 32), ([700, 130], 200, 16), ([9000], NO_WINDOW, 32)])
+def test_decode_fp8_infinite_values(h, pos, window, page, dh, size):
+    """Infinite and NaN values in FP8 pages: their channels are infinite or NaN whatever the weights (all below a half),
+    the others are as without them; the same on the tensor cores (dh 64, 128) and the CUDA cores (96)."""
+    H, Hkv = 16, 2
+    c = Paged(h, pos, H, Hkv, dh, window, 2, page, "bf16", True, seed=23)
+    last = [x - 9 for x in pos]
+    for b, x in enumerate(last):
+        n = 3
+        at = torch.arange(x, x + n, dtype=torch.int32, device="cuda")
+        g = gen(24 + b)
+        k, v = randn(g, n, Hkv, dh) * 0.25, randn(g, n, Hkv, dh) * size
+        v[0, :, 3], v[1, :, 40], v[0, :, 41] = math.inf, -math.inf, math.inf
+        v[0, :, 50], v[2, :, 50] = math.inf, -math.inf          # both signs: NaN
+        v[0, 0, 60], v[0, 0, 61] = math.nan, math.inf
+        v[2, 1, 7] = math.nan                                    # in a block without infinities
+        h.swa_page_append(c.p, c.pages, at, k.view(n, -1), v.view(n, -1), torch.full_like(at, b))
+    if size < 1:                                                 # every other value as small
+        for b, x in enumerate(pos):
+            at = torch.tensor([t for t in range(x + 1) if not last[b] <= t < last[b] + 3], dtype=torch.int32, device="cuda")
+            h.swa_page_append(c.p, c.pages, at, c.k[b, at.long()].reshape(len(at), -1),
+                              (c.v[b, at.long()] * size).reshape(len(at), -1), torch.full_like(at, b))
+    out = c.decode().view(len(pos), H, dh)
+    k, v = (rows_of(x, c.n_pages, Hkv, page, dh, True) for x in c.pools)
+    v = v.float().double()                                       # 448 x 2^120 is infinite in 32 bits
+    for b, x in enumerate(pos):
+        j = torch.arange(x + 1, device="cuda")
+        ids = c.table[b, j // page].long()
+        kk, vv = (t[ids, :, j % page] for t in (k, v))
+        mask = seen_mask(torch.tensor([x], device="cuda"), x + 1, window, 2)
+        seen = vv[mask[0]].repeat_interleave(H // Hkv, 1)        # [n, H, dh]
+        up, down, nan = (seen == math.inf).any(0), (seen == -math.inf).any(0), torch.isnan(seen).any(0)
+        want = torch.where(nan | (up & down), 2.0, up.double() - down.double())
+        assert torch.equal(class_of(out[b]), want)
+        assert want[0, 3] == 1 and want[0, 40] == -1 and want[0, 41] == 1 and want[0, 50] == 2 and want[0, 60] == 2
+        fine = torch.where(want == 0, out[b].double(), 0.0)
+        vv = torch.where((want == 0).view(Hkv, H // Hkv, dh)[:, 0], vv.nan_to_num(0, 0, 0), 0.0)
+        check(fine.view(1, -1), c.q[b:b + 1].view(1, H, dh), kk, vv, mask, c.p.scale, "bf16", f"sequence {b}")
