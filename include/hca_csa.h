@@ -436,7 +436,7 @@ hcsa_status swa_decode_attend(const hcsa_params *p, const hcsa_pages *pages, con
  *   y8 or NULL (bf16 layers, D a multiple of 32): y in the FP8 layout of hcsa_params.lowprec: rows x D
  *      bytes of E4M3 codes, then rows x D/32 int8 exponents, rounded once from y (not from its bf16 value);
  *      each exponent is the one of the exact y even where a block's maximum lies next to a power-of-two
- *      border, and is held to [-126, 120].
+ *      border, and is held to [-126, 120] (0 for a block of zeros, 120 for one with an infinite value or of NaN alone).
  * One of y and y8 at least; D at most 16384.  Reads p->D and p->dtype only. */
 hcsa_status hcsa_add_rmsnorm(const hcsa_params *p, int64_t rows, const void *x, int64_t ld_x, const void *delta,
                              int64_t ld_delta, const void *w, float eps, void *x_out, int64_t ld_xo, void *y,

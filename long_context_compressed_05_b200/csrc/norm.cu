@@ -59,8 +59,22 @@ __device__ __noinline__ double exact_rstd(const NormArgs &a, int64_t row, bool l
         }
     return 1 / sqrt(row_sum(sum, tpr, sub, red) / a.D + (double)a.eps);
 }
-// The row's exponents once more from the maxima in fp64, and the codes of the blocks whose exponent changes; each
-// thread reads its own vectors of x and delta again.
+// A block's maximum in fp32, over its four lanes of `lanes`; NaN only where all 32 values are.
+__device__ __forceinline__ float row_block_amax(const float *v, unsigned lanes) {
+    float a = fmaxf(fabsf(v[0]), fabsf(v[1]));
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) a = fmaxf(a, fmaxf(fabsf(v[i]), fabsf(v[i + 1])));
+    a = fmaxf(a, __shfl_xor_sync(lanes, a, 1));
+    return fmaxf(a, __shfl_xor_sync(lanes, a, 2));
+}
+// Does the exponent e of a block hang on the last bits of its maximum?  amax / 2^e lies in (224, 448] unless e is held,
+// or the block has no finite value but zero: those have nothing to decide.
+__device__ __forceinline__ bool at_border(float amax, int e) {
+    const float f = amax * lp::pow2f(-e);
+    return fabsf(f - 448.f) < 448.f * 0x1p-18f || fabsf(f - 224.f) < 224.f * 0x1p-18f;
+}
+// The exponents of the row's blocks at a border once more from the maxima in fp64, and the codes where the exponent
+// changes; each thread reads its own vectors of x and delta again.
 template <typename S>
 __device__ __noinline__ void exact_blocks(const NormArgs &a, int64_t row, bool live, int tid, int tpr, int sub, float rstd,
                                           double *red) {
@@ -81,22 +95,15 @@ __device__ __noinline__ void exact_blocks(const NormArgs &a, int64_t row, bool l
         const unsigned grp = 0xFu << (threadIdx.x & 28);
         big = fmax(big, __shfl_xor_sync(grp, big, 1));
         big = fmax(big, __shfl_xor_sync(grp, big, 2));
-        const int was = page_exponent(lp::block_amax(y));
+        const float amax = row_block_amax(y, grp);
+        const int was = page_exponent(amax);
+        if (!at_border(amax, was)) continue;
         const double at = ldexp(448.0, was);   // the fp32 exponent is right or one off
-        const int e = big > at ? was + 1 : big <= 0.5 * at && was > -126 ? was - 1 : was;
+        const int e = big > at && was < 120 ? was + 1 : big <= 0.5 * at && was > -126 ? was - 1 : was;
         if (e == was) continue;
         *reinterpret_cast<uint2 *>(codes + c) = codes_of(y, e);
         if ((c & 31) == 0) exps[c / 32] = (int8_t)e;
     }
-}
-
-// lp::block_amax where the whole warp calls it (a partial mask costs a warp synchronisation per shuffle)
-__device__ __forceinline__ float warp_block_amax(const float *v) {
-    float a = fmaxf(fabsf(v[0]), fabsf(v[1]));
-#pragma unroll
-    for (int i = 2; i < 8; i += 2) a = fmaxf(a, fmaxf(fabsf(v[i]), fabsf(v[i + 1])));
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    return fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
 }
 
 template <typename S, int VPT, bool FP8>
@@ -163,10 +170,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(NormArgs a, int tpr) 
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {   // D % 32 == 0: the four lanes of a block are in or out together
             const int c = tid + i * tpr;
-            const float amax = warp_block_amax(v[i]);
+            const float amax = row_block_amax(v[i], 0xffffffffu);   // (a partial mask would cost a synchronisation per shuffle)
             const int e = page_exponent(amax);
-            const float f = amax * lp::pow2f(-e);   // (224, 448] unless held or zero
-            near |= f > 448.f - 448.f * 0x1p-18f || fabsf(f - 224.f) < 224.f * 0x1p-18f;
+            near |= at_border(amax, e);
             if (live && c < nvec) {
                 *reinterpret_cast<uint2 *>(codes + row * a.D + c * V) = codes_of(v[i], e);
                 if ((c & 3) == 0) exps[row * (a.D / 32) + c / 4] = (int8_t)e;

@@ -788,3 +788,31 @@ def test_decode_fp8_infinite_values(h, pos, window, page, dh, size):
         fine = torch.where(want == 0, out[b].double(), 0.0)
         vv = torch.where((want == 0).view(Hkv, H // Hkv, dh)[:, 0], vv.nan_to_num(0, 0, 0), 0.0)
         check(fine.view(1, -1), c.q[b:b + 1].view(1, H, dh), kk, vv, mask, c.p.scale, "bf16", f"sequence {b}")
+
+
+@pytest.mark.parametrize("D", [160, 512, 2048, 8192])
+def test_norm_fp8_exponents_beside_a_border(h, D):
+    """Blocks of zeros, of NaN, infinite ones and ones past the exponent range have the exponent of their own values,
+    whether or not another block of the row, or a row next to it, lies at a power-of-two border."""
+    x = torch.ones(6, D, dtype=torch.bfloat16, device="cuda")
+    x[1, 3], x[2, 5] = math.nan, math.inf          # all of the row NaN; one channel NaN, the others zero
+    x[3] = 0
+    x[4, D // 2:] = 0
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    w[32:64] = 0
+    w[64:96] = math.inf
+    w[96:128] = torch.finfo(torch.bfloat16).max    # y up to 1.5 times it: past fp32 in row 4
+    w[128:160] = 2.0 ** -133
+    p = h.make_params(D=D)
+    for border in (1.0, 1.75):                     # 1.75: y just below 448 / 2^8 in each row of ones
+        w[:32] = border
+        y8 = torch.zeros(6 * (D + D // 32), dtype=torch.uint8, device="cuda")
+        h.hcsa_add_rmsnorm(p, x, None, w, 1e-12, None, None, y8)
+        got = y8[6 * D:].view(torch.int8).view(6, D // 32).double()
+        s = x.double()
+        y = (s / (s.square().mean(-1, keepdim=True) + 1e-12).sqrt() * w.double()).view(6, D // 32, 32).abs()
+        amax = y.nan_to_num(0, math.inf, -math.inf).amax(-1)
+        e = torch.ceil(torch.log2(amax / 448))
+        e = torch.where(amax > 448 * torch.exp2(e), e + 1, torch.where(amax <= 224 * torch.exp2(e), e - 1, e))
+        e = torch.where(torch.isnan(y).all(-1) | torch.isinf(amax), 120.0, torch.where(amax == 0, 0.0, e.clamp(-126, 120)))
+        assert torch.equal(got, e), (border, (got != e).nonzero().tolist())
