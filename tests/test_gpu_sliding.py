@@ -816,3 +816,25 @@ def test_norm_fp8_exponents_beside_a_border(h, D):
         e = torch.where(amax > 448 * torch.exp2(e), e + 1, torch.where(amax <= 224 * torch.exp2(e), e - 1, e))
         e = torch.where(torch.isnan(y).all(-1) | torch.isinf(amax), 120.0, torch.where(amax == 0, 0.0, e.clamp(-126, 120)))
         assert torch.equal(got, e), (border, (got != e).nonzero().tolist())
+
+
+@pytest.mark.parametrize("dh,Hkv", [(128, 1), (64, 2)])
+def test_attend_a_late_bad_value_of_a_long_sequence(h, dh, Hkv):
+    """One NaN near the end of a long causal sequence: the rows in front of it that share its block, each with more than
+    131000 keys, are as without it, and so is every block that its CTA takes later."""
+    T, H, bad = 131072, 2 * Hkv, 131069
+    g = gen(101)
+    q, k, v = (randn(g, T, n * dh) for n in (H, Hkv, Hkv))
+    v[bad, dh // 2] = math.nan                       # head 0
+    out = torch.full_like(q, math.nan)
+    h.swa_attend(attend_params(h, T, H, Hkv, dh, NO_WINDOW, 0, "bf16"), q, k, v, out)
+    torch.cuda.synchronize()
+    assert h.hcsa_get_device_status() == 0
+    got = out.view(T, Hkv, 2, dh)
+    assert torch.isnan(got[bad:, 0, :, dh // 2]).all()
+    got[bad:, 0, :, dh // 2] = 0
+    v[bad, dh // 2] = 0
+    assert torch.isfinite(out.float()).all()
+    for rows in (torch.arange(T - 140, bad, 7, device="cuda"), torch.arange(70000, 70016, device="cuda")):
+        mask = seen_mask(rows, T, NO_WINDOW, 0)
+        check(out[rows], q[rows].view(-1, H, dh), k.view(T, Hkv, dh), v.view(T, Hkv, dh), mask, dh ** -0.5, "bf16")
