@@ -208,20 +208,20 @@ __device__ __forceinline__ int nth_unit(const Args &p, int k) {
     return u < p.n_units ? (int)u : -1;
 }
 
-// Rows of this CTA's blocks that came out non-finite by a value that they do not see, over exactly their keys.  Runs after the
-// last block, when no warp waits any more: a row of a long sequence takes as long as it has keys, and the waits of
-// the pipeline are bounded.  By warp w of the eight softmax warps.
+// Rows of sub-tile s, lanes [32 quad, 32 quad + 32), of this CTA's blocks that came out non-finite by a value that they do
+// not see, over exactly their keys.  By the warp that has stored them, once it has handed over its last block: nothing
+// waits for it any more.  (A row of a long sequence takes as long as it has keys; the pipeline's waits are bounded.)
 template <int DH>
-__device__ __noinline__ void redo_rows(const Args &p, int w, int lane) {
+__device__ __noinline__ void redo_rows(const Args &p, int s, int quad, int lane) {
     const SwaArgs &a = p.a;
     for (int k = 0;; ++k) {
         const int u = nth_unit(p, k);
         if (u < 0) break;
         const Unit x = unit_of(p, u);
         const int behind = min(a.row1, x.w0 + x.c.n_tiles * kKT - x.c.pad);   // tokens loaded for the block
-        for (int r = w; r < 2 * kRows; r += 8) {
-            const int s = r / kRows, tl = r % kRows / p.G, t = x.first(s, p.tb) + tl, h = x.g * p.G + r % kRows % p.G;
-            if (tl >= p.tb || t > x.last(s, p.tb)) continue;
+        for (int r = 32 * quad; r < 32 * quad + 32; ++r) {
+            const int tl = r / p.G, t = x.first(s, p.tb) + tl, h = x.g * p.G + r - tl * p.G;
+            if (tl >= p.tb || t > x.last(s, p.tb)) break;
             const __nv_bfloat16 *o = (const __nv_bfloat16 *)a.out + (int64_t)t * a.ld_out + (int64_t)h * DH;
             bool fine = true;
             for (int d = lane; d < DH; d += 32) fine = fine && fabsf((float)o[d]) < INFINITY;
@@ -248,12 +248,10 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     extern __shared__ uint8_t smem_raw[];
     Bars<NST> *bars = reinterpret_cast<Bars<NST> *>(smem_raw);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 1);
-    volatile uint32_t *redo = tmem_slot + 1;   // a row of this CTA came out non-finite
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(tmem_slot + 4) + 1023) & ~uintptr_t(1023));
     const uint32_t Qs = tc::smem_u32(base), Ks = Qs + 2 * Sz::kTile, Vs = Ks + NST * Sz::kTile;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        *redo = 0;
         for (int i = 0; i < NST; ++i) {
             tc::mbar_init(&bars->k_full[i], 1);
             tc::mbar_init(&bars->k_empty[i], 2);   // both issuers
@@ -428,6 +426,7 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), tS = lanes + s * 128, tO = lanes + kColO + s * 128;
         const int tl = r / p.G, hh = r - tl * p.G;
         uint32_t ns = 0, nu = 0;     // steps and blocks seen
+        bool bad = false;            // an output of this thread's rows is not finite
         for (int kk = 0; ok; ++kk) {
             const int u = nth_unit(p, kk);
             if (u < 0) break;
@@ -597,13 +596,14 @@ swa_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             }
             float z0, z1;
             unf2(zero, z0, z1);
-            if (row_ok && z0 + z1 != 0.f) *redo = 1;   // looked at after the last block
+            bad = bad || (row_ok && z0 + z1 != 0.f);   // looked at after the last block
         }
+        __syncwarp();                // the rows as their threads have stored them
+        if (ok && __any_sync(0xffffffffu, bad)) redo_rows<DH>(p, s, quad, lane);
     }
     tc::tc_fence_before();
     __syncthreads();
     if (warp == 0) tc::tmem_free(tmem, 512);
-    if (warp >= 4 && ok && *redo) redo_rows<DH>(p, warp - 4, lane);
 }
 
 template <int DH>
