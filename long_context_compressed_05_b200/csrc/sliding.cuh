@@ -67,94 +67,6 @@ __device__ __forceinline__ bool column_seen(const BlockKeys &b, int c, int t, in
     return j <= t && (j > t - window || j < sinks);
 }
 
-// The blocked kernels give every masked key the weight 0, and 0 times a masked value that is infinite or NaN
-// is NaN.  So a row that comes out non-finite is looked at again by one warp: if a value that its block
-// loaded and the row does not see is non-finite (values_bad), and the row's own values do not account for
-// it (row_explained), the row is computed once more over exactly its keys (attend_row); else it is
-// non-finite by its own keys and values and stays.  A row that needs it sees no bad value in some bad channel,
-// so however many values are bad, only rows within a tile of one are computed twice.
-
-// Is a value of key head g in tokens [lo, hi) infinite or NaN?
-template <typename S>
-__device__ bool values_bad(const SwaArgs &a, int g, int64_t lo, int64_t hi, int lane) {
-    bool bad = false;
-    for (int64_t j = lo; j < hi; ++j) {
-        const S *v = (const S *)a.v + j * a.ld_v + (int64_t)g * a.dh;
-        for (int d = lane; d < a.dh; d += 32) bad = bad || !(fabsf((float)v[d]) < INFINITY);
-    }
-    return __any_sync(0xffffffffu, bad);
-}
-// Does every non-finite channel of the stored row (t, h) have a non-finite value among those the row sees?  Newest tokens
-// first: where many are bad, the first ones settle it.
-template <typename S>
-__device__ bool row_explained(const SwaArgs &a, int t, int h, int lane, int d0, int d1) {
-    const int g = h / (a.H / a.Hkv);
-    const S *o = (const S *)a.out + (int64_t)t * a.ld_out + (int64_t)h * a.dh;
-    unsigned open = 0;   // bit i: channel lane + 32 i is non-finite and not accounted for
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int d = lane + 32 * i;
-        if (d >= d0 && d < d1 && !(fabsf((float)o[d]) < INFINITY)) open |= 1u << i;
-    }
-    const int w0 = t - a.window + 1 > 0 ? t - a.window + 1 : 0, ns = a.sinks < w0 ? a.sinks : w0;
-    const int64_t n = (int64_t)ns + (t - w0 + 1);
-    for (int64_t c = n - 1; c >= 0 && __any_sync(0xffffffffu, open); --c) {
-        const int64_t j = c < ns ? c : w0 + (c - ns);
-        const S *v = (const S *)a.v + j * a.ld_v + (int64_t)g * a.dh;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if ((open >> i & 1) && !(fabsf((float)v[lane + 32 * i]) < INFINITY)) open &= ~(1u << i);
-    }
-    return !__any_sync(0xffffffffu, open);
-}
-// Row (t, h) over exactly the keys it sees, by one warp; channels [d0, d1) are stored.  Ends
-// early once every channel is NaN, which no further key can change.
-template <typename S>
-__device__ void attend_row(const SwaArgs &a, int t, int h, int lane, int d0, int d1) {
-    const int g = h / (a.H / a.Hkv);
-    const S *q = (const S *)a.q + (int64_t)t * a.ld_q + (int64_t)h * a.dh;
-    const S *k = (const S *)a.k + (int64_t)g * a.dh;
-    const S *v = (const S *)a.v + (int64_t)g * a.dh;
-    float acc[16], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    const int w0 = t - a.window + 1 > 0 ? t - a.window + 1 : 0;
-    const int ns = a.sinks < w0 ? a.sinks : w0;
-    for (int64_t c = 0; c < (int64_t)ns + (t - w0 + 1); ++c) {
-        const int64_t j = c < ns ? c : w0 + (c - ns);
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int d = lane + 32 * i;
-            if (d < a.dh) s += (float)q[d] * (float)k[j * a.ld_k + d];
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= a.scale * 1.4426950408889634f;
-        const float mn = fmaxf(m, s);
-        const float f = mn == -INFINITY ? 1.f : exp2f(m - mn);
-        const float p = s == -INFINITY && mn == -INFINITY ? 0.f : exp2f(s - mn);
-        m = mn;
-        l = l * f + p;
-        bool lost = true;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int d = lane + 32 * i;
-            if (d < a.dh) {
-                acc[i] = acc[i] * f + p * (float)v[j * a.ld_v + d];
-                lost = lost && acc[i] != acc[i];
-            }
-        }
-        if (__all_sync(0xffffffffu, lost || l != l)) break;
-    }
-    S *o = (S *)a.out + (int64_t)t * a.ld_out + (int64_t)h * a.dh;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int d = lane + 32 * i;
-        if (d >= d0 && d < d1) store_val(o + d, acc[i] / l);
-    }
-}
-
 // ---------------------------------------------------------------- paged cache
 struct PageArgs {
     int dtype;

@@ -24,7 +24,6 @@ struct SimtSmem {
     };
     float q[BM][DH + 4];
     Tile t[groups_of<DH>()];
-    int bad[BM];
 };
 
 template <typename S, int DH, int BM, int BN>
@@ -75,19 +74,9 @@ __global__ void __launch_bounds__(kThreads * groups_of<DH>(), DH <= 64 ? 2 : DH 
         return (const S *)a.q + (int64_t)(t_first + t) * a.ld_q + (int64_t)(g * G + x - t * G) * a.dh;
     });
 
-    float o[RM][DN][4], m[RM], l[RM];
     int tok[RM];
 #pragma unroll
-    for (int i = 0; i < RM; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-        const int r = ty + 16 * i;
-        tok[i] = r < n_rows ? t_first + (rem + r) / G : -1;
-#pragma unroll
-        for (int j = 0; j < DN; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
-    }
+    for (int i = 0; i < RM; ++i) tok[i] = ty + 16 * i < n_rows ? t_first + (rem + ty + 16 * i) / G : -1;
     // K and V of the next tile wait in registers while this one is worked on
     constexpr int NL = BN * (DH / V) / kThreads;
     static_assert(BN * (DH / V) % kThreads == 0, "whole vectors per thread");
@@ -105,23 +94,41 @@ __global__ void __launch_bounds__(kThreads * groups_of<DH>(), DH <= 64 ? 2 : DH 
             }
         }
     };
-    auto widen = [](const uint4 &raw, float *dst) {
+    auto widen = [](const uint4 &raw, float *dst, bool finite) {
         const S *e8 = reinterpret_cast<const S *>(&raw);
+        float f[V];
 #pragma unroll
-        for (int e = 0; e < V; e += 4)
-            *reinterpret_cast<float4 *>(dst + e) =
-                make_float4((float)e8[e], (float)e8[e + 1], (float)e8[e + 2], (float)e8[e + 3]);
+        for (int e = 0; e < V; ++e) f[e] = (float)e8[e];
+        if (finite) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) f[e] = fabsf(f[e]) < INFINITY ? f[e] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < V; e += 4) *reinterpret_cast<float4 *>(dst + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
     };
+    // Every masked key has the weight 0, and 0 times an infinite or NaN value is NaN.  So a block with a row that came
+    // out non-finite is computed a second time without such values, which then reach the rows that see them
+    for (int again = 0;; again = 1) {
+    float o[RM][DN][4], m[RM], l[RM];
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < DN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
+    }
     if (kAhead) fetch(group * BN);
-    __syncthreads();       // Q
+    __syncthreads();       // Q, or the first pass's last readers
     for (int c0 = group * BN; c0 < bk.n; c0 += NG * BN) {
         sync_group();      // the previous tile's readers are done
         if (!kAhead) fetch(c0);
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
             const int i = j * kThreads + tid, r = i / (DH / V), d = (i % (DH / V)) * V;
-            widen(kr[j], &tile.k[r][d]);
-            widen(vr[j], &tile.v[r][d]);
+            widen(kr[j], &tile.k[r][d], false);
+            widen(vr[j], &tile.v[r][d], again);
         }
         if (kAhead && c0 + NG * BN < bk.n) fetch(c0 + NG * BN);
         sync_group();
@@ -195,7 +202,6 @@ __global__ void __launch_bounds__(kThreads * groups_of<DH>(), DH <= 64 ? 2 : DH 
                 }
         }
     }
-    if (threadIdx.x < BM) sm.bad[threadIdx.x] = 0;
 #pragma unroll
     for (int i = 0; i < RM; ++i)
 #pragma unroll
@@ -228,11 +234,12 @@ __global__ void __launch_bounds__(kThreads * groups_of<DH>(), DH <= 64 ? 2 : DH 
             }
         }
     }
+    bool fine = true;
+    auto row = [&](int i) { return (S *)a.out + (int64_t)tok[i] * a.ld_out + (int64_t)(g * G + (rem + ty + 16 * i) % G) * a.dh; };
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
         if (tok[i] < 0 || group) continue;
-        S *dst = (S *)a.out + (int64_t)tok[i] * a.ld_out + (int64_t)(g * G + (rem + ty + 16 * i) % G) * a.dh;
-        bool fine = true;
+        S *dst = row(i);
 #pragma unroll
         for (int j = 0; j < DN; ++j) {
             const int d = 4 * tx + 32 * j;
@@ -243,16 +250,45 @@ __global__ void __launch_bounds__(kThreads * groups_of<DH>(), DH <= 64 ? 2 : DH 
                 if (d + e < a.dh) store_val(dst + d + e, y);
             }
         }
-        if (!fine) sm.bad[ty + 16 * i] = 1;
     }
-    __syncthreads();
-    const int lane = threadIdx.x & 31;
-    for (int r = threadIdx.x >> 5; r < BM; r += kThreads * NG / 32) {
-        if (!sm.bad[r]) continue;
-        const int t = t_first + (rem + r) / G, h = g * G + (rem + r) % G;
-        if ((values_bad<S>(a, g, bk.w0, (int64_t)t - a.window + 1, lane) || values_bad<S>(a, g, t + 1, t_end + 1, lane)) &&
-            !row_explained<S>(a, t, h, lane, 0, a.dh))
-            attend_row<S>(a, t, h, lane, 0, a.dh);
+    if (again) {
+        // infinite values that each row sees, by sign (NaN: both), a bit per channel: one sign makes the channel infinite, both
+        // NaN; a row whose weights are NaN stays so
+        using Bits = uint64_t;
+        static_assert(4 * DN <= 64, "a bit per channel");
+        Bits up[RM], down[RM];
+#pragma unroll
+        for (int i = 0; i < RM; ++i) up[i] = down[i] = 0;
+        for (int c = 0; c < bk.n && !group; ++c) {
+            const S *v = (const S *)a.v + (int64_t)bk.token(c) * a.ld_v + (int64_t)g * a.dh;
+            Bits u = 0, w = 0;
+#pragma unroll
+            for (int j = 0; j < 4 * DN; ++j) {
+                const int d = 4 * tx + 32 * (j / 4) + j % 4;
+                const float f = d < a.dh ? (float)v[d] : 0.f;
+                const Bits bit = fabsf(f) < INFINITY ? 0 : (Bits)1 << j;
+                if (!(f < 0.f)) u |= bit;
+                if (!(f > 0.f)) w |= bit;
+            }
+            if (!(u | w)) continue;
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
+                if (column_seen(bk, c, tok[i], a.window, a.sinks)) {
+                    up[i] |= u;
+                    down[i] |= w;
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < RM; ++i) {
+            if (tok[i] < 0 || group || !(l[i] > 0.f)) continue;
+            for (Bits any = up[i] | down[i]; any; any &= any - 1) {
+                const int j = __ffsll(any) - 1;
+                const bool u = up[i] >> j & 1, w = down[i] >> j & 1;
+                store_val(row(i) + 4 * tx + 32 * (j / 4) + j % 4, u && w ? NAN : u ? INFINITY : -INFINITY);
+            }
+        }
+    }
+    if (again || !__syncthreads_or(!fine)) break;
     }
 }
 

@@ -208,9 +208,188 @@ __device__ __forceinline__ int nth_unit(const Args &p, int k) {
     return u < p.n_units ? (int)u : -1;
 }
 
-// Rows of sub-tile s, lanes [32 quad, 32 quad + 32), of this CTA's blocks that came out non-finite by a value that they do
-// not see, over exactly their keys.  By the warp that has stored them, once it has handed over its last block: nothing
-// waits for it any more.  (A row of a long sequence takes as long as it has keys; the pipeline's waits are bounded.)
+__device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// bits 15 and 31: which of a word's two bf16 is infinite or NaN (its exponent all ones: the sum carries)
+__device__ __forceinline__ uint32_t bad_halves(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+// 16 rows from row r0 of sub-tile s, those in `rows`, once more over the keys that they see, by one warp.  Infinite and
+// NaN values leave the product (as zeros) and reach the rows that see them at the end: an infinite channel if all that a
+// row sees there have one sign, else NaN.  Operands straight from global memory, 16 keys at a time; lane (gr, cq) of
+// a product reads dims cq DH/4 .. of its rows and keys, and channels gr DH/8 .. of its values, so that its words are
+// contiguous, and holds channels cq DH/4 .. of output rows gr and gr + 8.
+template <int DH>
+__device__ __forceinline__ void attend_rows(const Args &p, const Unit &x, int s, int r0, uint32_t rows, int lane) {
+    constexpr int NK = DH / 16, NJ = DH / 8, NO = DH / 4;   // steps over dims, products over channels, channels of a lane
+    constexpr uint32_t kAll = NO == 32 ? ~0u : (1u << (NO & 31)) - 1u;
+    using bf16 = __nv_bfloat16;
+    const SwaArgs &a = p.a;
+    const int gr = lane >> 2, cq = lane & 3;
+    const int t_min = x.first(s, p.tb) + (r0 + __ffs(rows) - 1) / p.G, t_max = x.first(s, p.tb) + (r0 + 31 - __clz(rows)) / p.G;
+    const int w_lo = t_min - a.window + 1 > 0 ? t_min - a.window + 1 : 0, far = a.sinks < w_lo ? a.sinks : w_lo;
+    const int n = far + (t_max - w_lo + 1);
+    auto token = [&](int c) -> int64_t { return c < far ? c : w_lo + (c - far); };
+    int t[2];                        // -1: not a row to compute
+    int64_t at[2];                   // head of the row, in q and out columns
+    uint32_t q[NK][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = r0 + gr + 8 * i;
+        t[i] = rows >> (gr + 8 * i) & 1 ? x.first(s, p.tb) + r / p.G : -1;
+        at[i] = (int64_t)(x.g * p.G + r % p.G) * DH;
+        const bf16 *src = (const bf16 *)a.q + (t[i] < 0 ? 0 : t[i] * a.ld_q + at[i]) + cq * NO;
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+            const uint2 w = t[i] < 0 ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2 *>(src + 4 * k));
+            q[k][i] = w.x;
+            q[k][2 + i] = w.y;
+        }
+    }
+    auto seen = [&](int i, int c) {
+        const int64_t j = token(c);
+        return c < n && j <= t[i] && (j > (int64_t)t[i] - a.window || j < a.sinks);
+    };
+    const bf16 *kb = (const bf16 *)a.k + x.g * DH + cq * NO, *vb = (const bf16 *)a.v + x.g * DH;
+    float o[NJ][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    uint32_t pos[2] = {0, 0}, neg[2] = {0, 0};   // a bit per channel of the lane: infinite values seen, by sign (NaN: both)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+    for (int c0 = 0; c0 < n; c0 += 16) {
+        auto row_of = [&](int c) { return token(c < n ? c : n - 1); };   // columns past the end weigh nothing
+        float sc[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[h][e] = 0.f;
+            const bf16 *src = kb + row_of(c0 + 8 * h + gr) * a.ld_k;
+#pragma unroll
+            for (int k = 0; k < NK; k += 2) {
+                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + 4 * k));
+                mma16816(sc[h], q[k], w.x, w.y);
+                mma16816(sc[h], q[k + 1], w.z, w.w);
+            }
+        }
+        uint32_t v[4][NJ / 2];       // keys 2 cq, 2 cq + 1, 2 cq + 8, 2 cq + 9
+        uint32_t any = 0;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const bf16 *src = vb + row_of(c0 + 2 * cq + (y & 1) + 8 * (y >> 1)) * a.ld_v + gr * NJ;
+#pragma unroll
+            for (int w = 0; w < NJ / 2; w += 4) {
+                const uint4 r = __ldg(reinterpret_cast<const uint4 *>(src + 2 * w));
+                v[y][w] = r.x;
+                v[y][w + 1] = r.y;
+                v[y][w + 2] = r.z;
+                v[y][w + 3] = r.w;
+            }
+#pragma unroll
+            for (int w = 0; w < NJ / 2; ++w) {
+                const uint32_t bad = bad_halves(v[y][w]);
+                v[y][w] &= ~((bad >> 15) * 0xFFFFu);
+                any |= bad;
+            }
+        }
+        if (__any_sync(0xffffffffu, any)) {
+            for (int c = c0; c < c0 + 16 && c < n; ++c) {
+                const bf16 *src = vb + token(c) * a.ld_v + cq * NO;
+                uint32_t up = 0, down = 0;
+#pragma unroll
+                for (int i = 0; i < NO; i += 8) {
+                    const uint4 r = __ldg(reinterpret_cast<const uint4 *>(src + i));
+                    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float f = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+                        const uint32_t bit = fabsf(f) < INFINITY ? 0u : 1u << (i + e);
+                        if (!(f < 0.f)) up |= bit;
+                        if (!(f > 0.f)) down |= bit;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (seen(i, c)) {
+                        pos[i] |= up;
+                        neg[i] |= down;
+                    }
+            }
+            // every row NaN in every channel: no further key changes that
+            if (__all_sync(0xffffffffu, (t[0] < 0 || (pos[0] & neg[0]) == kAll) && (t[1] < 0 || (pos[1] & neg[1]) == kAll))) break;
+        }
+        float mx[2] = {m[0], m[1]};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sc[h][e] = seen(e >> 1, c0 + 8 * h + 2 * cq + (e & 1)) ? sc[h][e] * p.scale_log2 : -INFINITY;
+                mx[e >> 1] = fmaxf(mx[e >> 1], sc[h][e]);
+            }
+        float f[2], ref[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+            f[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - mx[i]);
+            ref[i] = mx[i] == -INFINITY ? 0.f : mx[i];
+            m[i] = mx[i];
+            l[i] *= f[i];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sc[h][e] = ex2(sc[h][e] - ref[e >> 1]);
+                l[e >> 1] += sc[h][e];
+            }
+        const uint32_t pw[4] = {pack2(sc[0][0], sc[0][1]), pack2(sc[0][2], sc[0][3]), pack2(sc[1][0], sc[1][1]),
+                                pack2(sc[1][2], sc[1][3])};
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][e] *= f[e >> 1];
+            const uint32_t half = j & 1 ? 0x7632 : 0x5410;
+            mma16816(o[j], pw, __byte_perm(v[0][j / 2], v[1][j / 2], half), __byte_perm(v[2][j / 2], v[3][j / 2], half));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        const float li = 1.f / l[i];
+        // channel c of the lane: product c % NJ, column c / NJ of its pair
+        auto value = [&](int c) {
+            const float y = o[c % NJ][2 * i + c / NJ] * li;
+            const bool up = pos[i] >> c & 1, down = neg[i] >> c & 1;
+            return !(up || down) || !(l[i] > 0.f) ? y : up && down ? NAN : up ? INFINITY : -INFINITY;
+        };
+        if (t[i] < 0) continue;
+        bf16 *dst = (bf16 *)a.out + t[i] * a.ld_out + at[i] + cq * NO;
+#pragma unroll
+        for (int c = 0; c < NO; c += 8)
+            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(pack2(value(c), value(c + 1)), pack2(value(c + 2), value(c + 3)),
+                                                             pack2(value(c + 4), value(c + 5)), pack2(value(c + 6), value(c + 7)));
+    }
+}
+
+// Is a value of key head g in tokens [lo, hi) infinite or NaN?
+template <int DH>
+__device__ bool values_bad(const SwaArgs &a, int g, int64_t lo, int64_t hi, int lane) {
+    uint32_t bad = 0;
+    for (int64_t j = lo; j < hi; ++j)
+        for (int d = 2 * lane; d < DH; d += 64)
+            bad |= bad_halves(__ldg(reinterpret_cast<const uint32_t *>((const __nv_bfloat16 *)a.v + j * a.ld_v + g * DH + d)));
+    return __any_sync(0xffffffffu, bad);
+}
+
+// The products give every masked key the weight 0, and 0 times an infinite or NaN value is NaN.  So the rows of sub-tile s,
+// lanes [32 quad, 32 quad + 32), of this CTA's blocks that came out non-finite are computed again where a value that their
+// block loaded and not all of them see is infinite or NaN.  By the warp that has stored them, once it has handed over its
+// last block: nothing waits for it any more.  (Rows take as long as they have keys, the pipeline's waits are bounded.)
 template <int DH>
 __device__ __noinline__ void redo_rows(const Args &p, int s, int quad, int lane) {
     const SwaArgs &a = p.a;
@@ -218,20 +397,23 @@ __device__ __noinline__ void redo_rows(const Args &p, int s, int quad, int lane)
         const int u = nth_unit(p, k);
         if (u < 0) break;
         const Unit x = unit_of(p, u);
-        const int behind = min(a.row1, x.w0 + x.c.n_tiles * kKT - x.c.pad);   // tokens loaded for the block
-        for (int r = 32 * quad; r < 32 * quad + 32; ++r) {
-            const int tl = r / p.G, t = x.first(s, p.tb) + tl, h = x.g * p.G + r - tl * p.G;
+        uint32_t bad = 0;
+        for (int i = 0; i < 32; ++i) {
+            const int r = 32 * quad + i, tl = r / p.G, t = x.first(s, p.tb) + tl, h = x.g * p.G + r - tl * p.G;
             if (tl >= p.tb || t > x.last(s, p.tb)) break;
-            const __nv_bfloat16 *o = (const __nv_bfloat16 *)a.out + (int64_t)t * a.ld_out + (int64_t)h * DH;
-            bool fine = true;
-            for (int d = lane; d < DH; d += 32) fine = fine && fabsf((float)o[d]) < INFINITY;
-            if (__all_sync(0xffffffffu, fine)) continue;
-            if ((values_bad<__nv_bfloat16>(a, x.g, x.w0, (int64_t)t - a.window + 1, lane) ||
-                 values_bad<__nv_bfloat16>(a, x.g, t + 1, behind, lane) ||
-                 (x.c.pad && values_bad<__nv_bfloat16>(a, x.g, x.c.sk, x.c.pad, lane))) &&
-                !row_explained<__nv_bfloat16>(a, t, h, lane, 0, DH))
-                attend_row<__nv_bfloat16>(a, t, h, lane, 0, DH);
+            const uint32_t *o = reinterpret_cast<const uint32_t *>((const __nv_bfloat16 *)a.out + t * a.ld_out + (int64_t)h * DH);
+            uint32_t b = 0;
+            for (int d = lane; d < DH / 2; d += 32) b |= bad_halves(o[d]);
+            if (__any_sync(0xffffffffu, b)) bad |= 1u << i;
         }
+        if (!bad) continue;
+        const int ta = x.first(s, p.tb) + (32 * quad + __ffs(bad) - 1) / p.G, te = x.first(s, p.tb) + (32 * quad + 31 - __clz(bad)) / p.G;
+        const int behind = min(a.row1, x.w0 + x.c.n_tiles * kKT - x.c.pad);   // tokens loaded for the block
+        if (!values_bad<DH>(a, x.g, x.w0, (int64_t)te - a.window + 1, lane) && !values_bad<DH>(a, x.g, ta + 1, behind, lane) &&
+            !(x.c.pad && values_bad<DH>(a, x.g, x.c.sk, x.c.pad, lane)))
+            continue;
+        for (int half = 0; half < 2; ++half)
+            if (bad >> (16 * half) & 0xFFFFu) attend_rows<DH>(p, x, s, 32 * quad + 16 * half, bad >> (16 * half) & 0xFFFFu, lane);
     }
 }
 

@@ -838,3 +838,42 @@ def test_attend_a_late_bad_value_of_a_long_sequence(h, dh, Hkv):
     for rows in (torch.arange(T - 140, bad, 7, device="cuda"), torch.arange(70000, 70016, device="cuda")):
         mask = seen_mask(rows, T, NO_WINDOW, 0)
         check(out[rows], q[rows].view(-1, H, dh), k.view(T, Hkv, dh), v.view(T, Hkv, dh), mask, dh ** -0.5, "bf16")
+
+
+@pytest.mark.parametrize("dtype,H,Hkv,dh,window,sinks", [
+    ("bf16", 4, 2, 128, NO_WINDOW, 0), ("bf16", 8, 1, 64, 60, 5), ("bf16", 3, 1, 128, 128, 20), ("bf16", 1, 1, 64, 300, 0),
+    ("bf16", 128, 1, 64, 90, 3), ("f32", 4, 2, 64, NO_WINDOW, 0), ("f32", 2, 1, 128, 50, 7), ("f32", 3, 1, 200, 100, 2),
+    ("f32", 1, 1, 512, 40, 0), ("bf16", 5, 1, 72, 64, 3), ("bf16", 2, 1, 256, 33, 1)])
+def test_attend_infinite_values_by_what_a_row_sees(h, dtype, H, Hkv, dh, window, sinks):
+    """Each output is infinite with the sign, NaN or finite as the values that its row sees make it, whatever lies next to
+    them: infinities and NaN of the same channels at neighbouring tokens, of which a row sees some."""
+    T = 450
+    g = gen(111)
+    q, k, v = (randn(g, T, n * dh, dtype=dt(dtype)) for n in (H, Hkv, Hkv))
+    vv = v.view(T, Hkv, dh)
+    vv[100, :, 3], vv[103, :, 3] = math.inf, math.nan            # rows 100 .. 102: infinite
+    vv[200, :, 9], vv[207, :, 9] = -math.inf, math.inf           # rows 200 .. 206: infinite, then NaN, later infinite
+    vv[290, :, 17] = math.inf
+    vv[300:310, 0, 20:40] = math.nan
+    vv[8, :, 50], vv[12, :, 51], vv[2, :, 60], vv[6, :, 60] = math.inf, math.nan, math.inf, -math.inf
+    vv[T - 2, Hkv - 1, dh - 1] = -math.inf
+    k.view(T, Hkv, dh)[350, 0, 4] = math.nan                     # weights of the rows that see it
+    out = torch.empty_like(q)
+    p = attend_params(h, T, H, Hkv, dh, window, sinks, dtype)
+    h.swa_attend(p, q, k, v, out)
+    got = out.view(T, H, dh)
+    mask = seen_mask(torch.arange(T, device="cuda"), T, window, sinks)
+    see = mask.double()
+
+    def any_seen(x):                                             # [T, Hkv, dh] truth -> [T, H, dh]
+        return (torch.einsum("tj,jgd->tgd", see, x.double()) > 0).repeat_interleave(H // Hkv, 1)
+
+    up, down, nan = any_seen(vv == math.inf), any_seen(vv == -math.inf), any_seen(torch.isnan(vv))
+    lost = (mask[:, 350, None, None] & (torch.arange(H, device="cuda") < H // Hkv)[:, None]).expand(T, H, dh)
+    want = torch.where(nan | (up & down) | lost, 2.0, up.double() - down.double())
+    wrong = class_of(got) != want
+    assert not wrong.any(), (int(wrong.sum()), wrong.nonzero()[:5].tolist())
+    assert want[101, 0, 3] == 1 and want[204, 0, 9] == -1 and (want[1] == 0).all()
+    clean_k, clean_v = k.nan_to_num(0).view(T, Hkv, dh), torch.where(torch.isfinite(vv), vv, 0.0)
+    plain, _, _ = attend64(q.view(T, H, dh), clean_k, clean_v, mask, p.scale)
+    check(torch.where(want == 0, got.double(), plain), q.view(T, H, dh), clean_k, clean_v, mask, p.scale, dtype)
