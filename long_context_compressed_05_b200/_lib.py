@@ -339,9 +339,8 @@ def make_pages(k_pages, v_pages, page_table) -> Pages:
 
 
 # These calls check what the C library cannot see (element types, extents, strides, devices).  A decode step makes many
-# of them, so the checks are few attribute reads each and the stream comes from torch's raw accessors: about
-# 9 us a call on the host instead of 15, the launch included.
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# of them, so the checks are few attribute reads each and the stream comes from torch's raw accessors (looked up when
+# called: a torch without CUDA has none): about 9 us a call on the host instead of 15, the launch included.
 
 
 def _rows2d(fn, t, dtype, rows, cols):
@@ -379,11 +378,12 @@ def _call(fn, dev, stream, tensors, call, *args):
             raise HcsaError(fn, 2)
     if dev < 0:
         raise HcsaError(fn, 2)
-    if dev == _current_device():
-        code = call(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    at = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        code = call(*args, at)
     else:
         with torch.cuda.device(dev):
-            code = call(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+            code = call(*args, at)
     if code:
         raise HcsaError(fn, code)
 

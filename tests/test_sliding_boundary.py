@@ -175,3 +175,27 @@ def test_calls_of_no_rows_take_tensors_without_an_address(h):
     assert attend(h, params(h, T=0), q=0, k=0, v=0, out=0) == 0
     assert append(h, params(h), pages(h), rows=0, pos=0, k=0, v=0) == 0
     assert norm(h, h.make_params(D=256), rows=0, x=0, delta=0, xo=0, y=0) == 0
+
+
+def test_the_package_works_on_a_torch_without_cuda(h):
+    """Import, host-side checks and refusals where torch has none of its CUDA accessors."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+for n in [n for n in dir(torch._C) if n.startswith("_cuda_get")]:
+    delattr(torch._C, n)
+import long_context_compressed_05_b200 as h
+p = h.make_params(D=64)
+x = torch.zeros(3, 64, dtype=torch.bfloat16)
+try:
+    h.hcsa_add_rmsnorm(p, x, None, torch.ones(64, dtype=torch.bfloat16), 1e-6, None, x.clone())
+except h.HcsaError as e:
+    assert e.code == 2
+else:
+    raise SystemExit("CPU tensors were taken")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
