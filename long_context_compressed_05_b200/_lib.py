@@ -329,10 +329,11 @@ def make_pages(k_pages, v_pages, page_table) -> Pages:
         raise HcsaError("make_pages", 2)
     pages = Pages(k_pages=_ptr(k_pages), v_pages=_ptr(v_pages), page_table=_ptr(page_table))
     pages.tensors = (k_pages, v_pages, page_table)
-    # what the calls check: element type, bytes of the smaller array, entries of the table, device
+    # what the calls check: element type, bytes of the smaller array, entries and row length of the table, device
     pages.dtype = k_pages.dtype if k_pages.dtype == v_pages.dtype else None
     pages.bytes = min(t.numel() * t.element_size() for t in (k_pages, v_pages))
     pages.entries = page_table.numel()
+    pages.row = page_table.shape[1] if page_table.dim() == 2 and page_table.shape[0] > 1 else 0   # 0: any
     dev = {t.get_device() for t in pages.tensors}
     pages.device = dev.pop() if len(dev) == 1 else -1
     return pages
@@ -367,7 +368,7 @@ def _check_pages(fn, p, pages):
         raise HcsaError(fn, 3)
     rows, dh = p.n_pages * p.Hkv * p.page, p.dh
     if (pages.bytes < rows * (dh + dh // 32 if p.lowprec else dh * dt.itemsize)
-            or pages.entries < p.B * p.max_pages):
+            or pages.entries < p.B * p.max_pages or (p.B > 1 and pages.row not in (0, p.max_pages))):
         raise HcsaError(fn, 2)
 
 

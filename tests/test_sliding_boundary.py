@@ -199,3 +199,25 @@ else:
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_a_page_table_of_another_row_length_is_refused(h):
+    """Its entries would be read as other sequences' pages."""
+    p = params(h)                                             # B 4, max_pages 4
+    kp = torch.zeros(10, 2, 16, 64, dtype=torch.bfloat16)
+    pos = torch.zeros(4, dtype=torch.int32)
+    kv, q = torch.zeros(4, 128, dtype=torch.bfloat16), torch.zeros(4, 512, dtype=torch.bfloat16)
+    ws = torch.zeros(16, dtype=torch.uint8)
+    for shape, refused in (((4, 5), True), ((8, 2), True), ((4, 4), False), ((6, 4), False), ((16,), False)):
+        pages = h.make_pages(kp, kp, torch.zeros(shape, dtype=torch.int32))
+        from long_context_compressed_05_b200 import _lib
+        if not refused:
+            _lib._check_pages("test", p, pages)
+            continue
+        for call in (lambda: h.swa_page_append(p, pages, pos, kv, kv), lambda: h.swa_decode_attend(p, pages, pos, q, q, ws),
+                     lambda: _lib._check_pages("test", p, pages)):
+            with pytest.raises(h.HcsaError) as e:
+                call()
+            assert e.value.code == 2
+    one = params(h, B=1)                                      # a single sequence's table may be longer than it needs
+    _lib._check_pages("test", one, h.make_pages(kp, kp, torch.zeros(1, 9, dtype=torch.int32)))
