@@ -352,7 +352,7 @@ def _rows2d(fn, t, dtype, rows, cols):
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[0] < rows or shape[1] != cols or (stride[1] != 1 and cols > 1):
         raise HcsaError(fn, 2)
-    return stride[0] if shape[0] > 1 else max(cols, stride[0])
+    return stride[0] if rows > 1 else cols
 
 
 def _vec32(fn, t, n):

@@ -877,3 +877,23 @@ def test_attend_infinite_values_by_what_a_row_sees(h, dtype, H, Hkv, dh, window,
     clean_k, clean_v = k.nan_to_num(0).view(T, Hkv, dh), torch.where(torch.isfinite(vv), vv, 0.0)
     plain, _, _ = attend64(q.view(T, H, dh), clean_k, clean_v, mask, p.scale)
     check(torch.where(want == 0, got.double(), plain), q.view(T, H, dh), clean_k, clean_v, mask, p.scale, dtype)
+
+
+def test_a_single_row_of_any_stride(h):
+    """One token's row out of a tensor whose rows are not multiples of 16 bytes apart: its stride is never used."""
+    g = gen(121)
+
+    def row(n):
+        return randn(g, 3, n + 5)[:1, :n]
+
+    x, y, w = row(256), row(256), randn(g, 256)
+    h.hcsa_add_rmsnorm(h.make_params(D=256), x, None, w, 1e-6, None, y)
+    want = x.double() / (x.double().square().mean(-1, keepdim=True) + 1e-6).sqrt() * w.double()
+    assert ((y.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -17) * want.abs()).all()
+    q, k, v, out = row(8 * 64), row(2 * 64), row(2 * 64), row(8 * 64)
+    h.swa_attend(attend_params(h, 1, 8, 2, 64, 5, 1, "bf16"), q, k, v, out)
+    assert torch.equal(out.view(2, 4, 64), v.view(2, 1, 64).expand(2, 4, 64))
+    c = Paged(h, [40], 8, 2, 64, NO_WINDOW, 0, 16, "bf16", seed=5)
+    h.swa_page_append(c.p, c.pages, c.pos, k, v)
+    c.q = row(8 * 64)
+    c.check(c.decode(out))
