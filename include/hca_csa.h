@@ -432,7 +432,8 @@ hcsa_status swa_decode_attend(const hcsa_params *p, const hcsa_pages *pages, con
  *     s = x + delta,  x_out = round(s),  y = s / sqrt(mean(s^2) + eps) * w
  * with s and the mean in fp32 or wider, each result rounded once.
  *   x [rows, ld_x]; delta [rows, ld_delta] or NULL (s = x); w [D]; x_out [rows, ld_xo] or NULL, may be x or delta itself
- *   y  [rows, ld_y] in p->dtype, or NULL; not x_out, and with y8 neither x nor delta
+ *   (with its leading dimension; outputs overlap nothing otherwise)
+ *   y  [rows, ld_y] in p->dtype, or NULL; may be x or delta itself without y8; not x_out
  *   y8 or NULL (bf16 layers, D a multiple of 32): y in the FP8 layout of hcsa_params.lowprec: rows x D
  *      bytes of E4M3 codes, then rows x D/32 int8 exponents, rounded once from y (not from its bf16 value);
  *      each exponent is the one of the exact y even where a block's maximum lies next to a power-of-two

@@ -625,6 +625,10 @@ hcsa_status hcsa_add_rmsnorm(const hcsa_params *p, int64_t rows, const void *x, 
     if (!ld_ok(p->dtype, ld_x, p->D) || (delta && !ld_ok(p->dtype, ld_delta, p->D)) ||
         (x_out && !ld_ok(p->dtype, ld_xo, p->D)) || (y && !ld_ok(p->dtype, ld_y, p->D)))
         return HCSA_ERR_ALIGN;
+    // an output over an input: each thread writes where it has read, which needs the same rows
+    if (rows > 1 && ((x_out && ((x_out == x && ld_xo != ld_x) || (x_out == delta && ld_xo != ld_delta))) ||
+                     (y && ((y == x && ld_y != ld_x) || (y == delta && ld_y != ld_delta)))))
+        return HCSA_ERR_UNSUPPORTED;
     // with y8, x and delta may be read again after y is stored
     if (rows && y && (y == x_out || (y8 && (y == x || y == delta)))) return HCSA_ERR_UNSUPPORTED;
     NormArgs a{p->dtype, rows, p->D, x, ld_x, delta, ld_delta, w, eps, x_out, ld_xo, y, ld_y, y8};

@@ -897,3 +897,18 @@ def test_a_single_row_of_any_stride(h):
     h.swa_page_append(c.p, c.pages, c.pos, k, v)
     c.q = row(8 * 64)
     c.check(c.decode(out))
+
+
+@pytest.mark.parametrize("dtype,rows,D", [("bf16", 3000, 416), ("f32", 70, 2048)])
+def test_norm_over_its_inputs(h, dtype, rows, D):
+    """y over x or over delta, x_out over the other one."""
+    g = gen(131)
+    x, d, w = (randn(g, *s, dtype=dt(dtype)) for s in ((rows, D), (rows, D), (D,)))
+    p = h.make_params(D=D, dtype=dtype)
+    xo, y = torch.empty_like(x), torch.empty_like(x)
+    h.hcsa_add_rmsnorm(p, x, d, w, 1e-6, xo, y)
+    for swap in (False, True):
+        a, b = x.clone(), d.clone()
+        h.hcsa_add_rmsnorm(p, a, b, w, 1e-6, *((b, a) if swap else (a, b)))
+        got = (b, a) if swap else (a, b)
+        assert torch.equal(got[0], xo) and torch.equal(got[1], y)

@@ -221,3 +221,13 @@ def test_a_page_table_of_another_row_length_is_refused(h):
             assert e.value.code == 2
     one = params(h, B=1)                                      # a single sequence's table may be longer than it needs
     _lib._check_pages("test", one, h.make_pages(kp, kp, torch.zeros(1, 9, dtype=torch.int32)))
+
+
+def test_norm_in_place_needs_the_same_leading_dimension(h):
+    """Rows of an output over an input's address that start elsewhere would be written before they are read."""
+    p = h.make_params(D=256)
+    other = 0x20000
+    assert norm(h, p, xo=FAKE, ld_xo=512, y=other) == 8                          # x_out over x
+    assert norm(h, p, delta=other, ld_d=512, xo=other, y=0x30000) == 8           # x_out over delta
+    assert norm(h, p, delta=0x30000, xo=0, y=FAKE, ld_y=264) == 8                # y over x
+    assert norm(h, p, delta=other, ld_d=512, xo=0, y=other) == 8                 # y over delta
