@@ -580,6 +580,7 @@ hcsa_status swa_attend(const hcsa_params *p, const void *q, int64_t ld_q, const 
     int64_t r0, r1;
     HCSA_TRY(row_range(p, &r0, &r1));
     if (r1 <= r0) return HCSA_OK;
+    if (out == q || out == k || out == v) return HCSA_ERR_UNSUPPORTED;   // read again after rows are stored
     SwaArgs a{p->dtype, p->T, p->H, p->Hkv, p->dh, p->window, p->sinks, p->scale, q, ld_q, k, ld_k, v, ld_v, out,
               ld_out, (int)r0, (int)r1, device_status_ptr()};
     return launch_swa(a, (cudaStream_t)stream);

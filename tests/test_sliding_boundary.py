@@ -231,3 +231,10 @@ def test_norm_in_place_needs_the_same_leading_dimension(h):
     assert norm(h, p, delta=other, ld_d=512, xo=other, y=0x30000) == 8           # x_out over delta
     assert norm(h, p, delta=0x30000, xo=0, y=FAKE, ld_y=264) == 8                # y over x
     assert norm(h, p, delta=other, ld_d=512, xo=0, y=other) == 8                 # y over delta
+
+
+def test_attend_refuses_an_output_over_its_inputs(h):
+    """Rows may be computed again after others are stored, so the inputs have to last."""
+    far = dict(q=0x20000, k=0x30000, v=0x40000)
+    for name in ("q", "k", "v"):
+        assert attend(h, params(h), **{**far, name: FAKE}) == 8
