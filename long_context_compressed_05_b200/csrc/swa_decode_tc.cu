@@ -612,8 +612,8 @@ swa_decode_tc_kernel(DecodeArgs a, Split s, const __grid_constant__ CUtensorMap 
             if (__any_sync(0xffffffffu, lane < 2 * NB && sm_cls[warp][lane % (2 * NB)]))
                 for (int b = 0; b < NB; ++b) {
                     const bool pos = sm_cls[warp][b] >> lane & 1, neg = sm_cls[warp][NB + b] >> lane & 1;
-                    for (int h = 0; (pos || neg) && h < kHB; ++h)
-                        acc[(warp * kHB + h) * DH + 32 * b + lane] = pos && neg ? NAN : pos ? INFINITY : -INFINITY;
+                    for (int h = 0; (pos || neg) && h < kHB; ++h)   // added: a channel that is NaN already stays so
+                        acc[(warp * kHB + h) * DH + 32 * b + lane] += pos && neg ? NAN : pos ? INFINITY : -INFINITY;
                 }
         }
         __syncthreads();

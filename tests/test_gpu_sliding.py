@@ -912,3 +912,18 @@ def test_norm_over_its_inputs(h, dtype, rows, D):
         h.hcsa_add_rmsnorm(p, a, b, w, 1e-6, *((b, a) if swap else (a, b)))
         got = (b, a) if swap else (a, b)
         assert torch.equal(got[0], xo) and torch.equal(got[1], y)
+
+
+@pytest.mark.parametrize("dh", [64, 96, 128])
+def test_decode_fp8_nan_and_infinity_in_one_channel(h, dh):
+    """A NaN in a block of ordinary values and an infinite value of the same channel in another token: NaN."""
+    n = 60
+    c = Paged(h, [n - 1], 4, 1, dh, NO_WINDOW, 0, 32, "bf16", True, seed=29)
+    v = c.v[0].clone()
+    v[50, 0, 5], v[20, 0, 5] = math.nan, -math.inf
+    v[50, 0, 40], v[51, 0, 40] = math.inf, math.nan
+    at = torch.arange(n, dtype=torch.int32, device="cuda")
+    h.swa_page_append(c.p, c.pages, at, c.k[0].view(n, -1), v.view(n, -1), torch.zeros_like(at))
+    got = c.decode().view(4, dh)
+    assert torch.isnan(got[:, 5]).all() and torch.isnan(got[:, 40]).all()
+    assert torch.isfinite(got[:, :5]).all() and torch.isfinite(got[:, 6:40]).all() and torch.isfinite(got[:, 41:]).all()
