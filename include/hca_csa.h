@@ -402,7 +402,7 @@ size_t hcsa_page_bytes(const hcsa_params *p);
  *   q [T, ld_q] (H*dh used, head-major), k [T, ld_k], v [T, ld_v] (Hkv*dh used each), out [T, ld_out] (H*dh
  *   columns written; it overlaps none of the inputs).  A key or value that no query of a row may see never
  *   reaches that row, whatever it holds (infinities and NaN included); an infinite value that a row sees makes its
- *   channel infinite, two of opposite signs or a NaN make it NaN. */
+ *   channel infinite, two of opposite signs or a NaN make it NaN (NaN also where the weight underflows fp32). */
 hcsa_status swa_attend(const hcsa_params *p, const void *q, int64_t ld_q, const void *k, int64_t ld_k,
                        const void *v, int64_t ld_v, void *out, int64_t ld_out, void *stream);
 

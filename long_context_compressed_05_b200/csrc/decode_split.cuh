@@ -13,7 +13,7 @@
 namespace hcsa {
 
 constexpr int kDirectTokens = 256;
-constexpr int kMinShare = 8;        // chunks: a smaller piece costs more to join than it saves
+constexpr int kMinShare = 8;        // chunks of a piece at least (128 tokens, 256 of FP8 pages of 32 k tokens)
 
 struct Split {
     int units_per_seq;              // key heads x head blocks
@@ -101,7 +101,7 @@ __device__ __forceinline__ Piece piece_of(const DecodeArgs &a, const Split &s, i
 
 size_t decode_split_bytes(int B, int grid, int heads, int dh);
 Split make_split(const DecodeArgs &a, int units_per_seq, int heads, int grid);
-// zero rows of empty slots and join the partials; heads: query heads per unit, blocks: head blocks per key head
+// zero rows of empty slots and join the partials; heads: query heads per unit, grid: CTAs of the split kernel
 hcsa_status launch_decode_join(const DecodeArgs &a, const Split &s, int heads, int grid, cudaStream_t st);
 bool decode_direct(const DecodeArgs &a);
 

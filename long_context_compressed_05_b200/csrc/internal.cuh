@@ -10,7 +10,8 @@
 namespace hcsa {
 
 // ---------------------------------------------------------------- storage / compute types
-// HCSA_F32 stores fp32 and computes in fp64; HCSA_BF16 stores bf16 and computes in fp32.
+// HCSA_F32 stores fp32 and computes in fp64 (the sliding-window calls and the norm: fp32); HCSA_BF16 stores bf16 and
+// computes in fp32.
 template <typename S> struct Traits;
 template <> struct Traits<float> {
     using A = double;

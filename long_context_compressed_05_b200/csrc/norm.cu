@@ -44,8 +44,8 @@ __device__ __forceinline__ T row_sum(T v, int tpr, int sub, T *red) {
 
 // The sum of squares is fp32: a thread's at most 32 values (in eight partial sums), then a tree of at most 10: y is
 // within 2^-19 of its exact value.  FP8: a block whose maximum lies within 2^-18 of a power-of-two border makes its
-// row sum once more in fp64 and takes the border's side from that; one row in a thousand has such a block.  (With
-// every sum in fp64, 131072 rows of 2048 took 778 us instead of 334.)
+// row sum once more in fp64 and takes the border's side from that; one row in a thousand has such a block.  (131072 rows
+// of 2048 took 833 us with every sum in fp64 and 427 when that went; later steps brought it to 315.)
 // The row's 1 / sqrt(mean + eps) in fp64, read again (out of line: it would double the kernel's registers).
 template <typename S>
 __device__ __noinline__ double exact_rstd(const NormArgs &a, int64_t row, bool live, int tid, int tpr, int sub, double *red) {
@@ -209,8 +209,8 @@ void launch_v(const NormArgs &a, int vpt, int tpr, cudaStream_t st) {
 hcsa_status launch_add_rmsnorm(const NormArgs &a, cudaStream_t st) {
     if (a.rows == 0) return HCSA_OK;
     const int nvec = a.D / (a.dtype == HCSA_BF16 ? 8 : 4);
-    // few rows: one vector per thread (the shortest path); many: up to four (131072 rows of 2048, FP8: 334 us; 537 with
-    // two, more threads to reduce over; 406 with eight, fewer warps per SM)
+    // few rows: one vector per thread (the shortest path); many: up to four (131072 rows of 2048, FP8, in a captured graph:
+    // 315 us; 424 with two, more threads to reduce over; 662 with eight, fewer warps per SM)
     int vpt = 1;
     while (vpt < 4 && ((a.rows > 1024 && vpt * 32 < nvec) || vpt * 1024 < nvec)) vpt *= 2;
     int tpr = 32;

@@ -2,8 +2,8 @@
 // Bandwidth- or launch-bound.  A block takes up to kRows rows: one thread per row finds where it goes (position, page,
 // bounds), then the block copies the rows' 16-byte vectors.  A thread keeps its column (so its head, channel and
 // addresses' strides are worked out once) and takes rows in turn, four in flight: with a flat index per vector the two
-// divisions and the addresses were half of the FP8 kernel's instructions (8191 rows of 8 heads of 128, FP8: 15.3 us
-// against 13.0).
+// divisions and the addresses were half of the FP8 kernel's instructions (8191 rows of 8 heads of 128, FP8, in a captured
+// graph: 15.3 us against 13.0 to 13.9; about 21 a call where the host makes them one by one).  In bf16 8.7 us.
 #include "sliding.cuh"
 
 namespace hcsa {
@@ -92,7 +92,8 @@ hcsa_status launch_page_append(const PageArgs &a, int64_t rows, const int32_t *p
     const int64_t nv64 = (int64_t)a.Hkv * a.dh / (a.dtype == HCSA_BF16 ? 8 : 4);
     if (nv64 > 1 << 23) return HCSA_ERR_UNSUPPORTED;
     const int nv = (int)nv64;
-    // rows per block: about two thousand vectors (13.0 us; a thousand 14.5, four thousand 14.0), fewer where the blocks would not fill the GPU
+    // rows per block: about two thousand vectors (FP8 as above: 13.0 us; a thousand 14.5, four thousand 14.0), fewer where the
+    // blocks would not fill the GPU
     int64_t per = 2048 / (2 * nv);
     const int64_t spread = rows / (4 * sm_grid(1));
     if (per > spread) per = spread;

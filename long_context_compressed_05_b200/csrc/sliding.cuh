@@ -1,5 +1,5 @@
 // Sliding-window layers: the key sets of prefill blocks and decode steps, the argument structs of the
-// launchers, and the exact recomputation of single rows.
+// launchers, and the exponents and codes of 8-bit rows.
 #pragma once
 
 #include "internal.cuh"

@@ -5,7 +5,7 @@
 // operands come from shared memory per warp: no CTA-wide step, no TMEM round trip, and 16 rows is what a group
 // of heads fills, where tcgen05 would run 128 rows for them.
 //
-// Four warps take the chunks (16 tokens; never across a page) of a CTA's segment in turn.  Each warp runs its own
+// Four warps take the chunks (16 tokens, or 32 of FP8 pages; never across a page) of a CTA's segment in turn.  Each warp runs its own
 // ring of stages: lane 0 asks for a chunk's K and V by TMA boxes (hardware swizzle, so that ldmatrix reads without
 // bank conflicts), 32 page ids are read at a time, and no warp waits for another until the segment's end, where
 // the four (max, sum, O) are joined through the ring's memory.
@@ -36,7 +36,9 @@ namespace {
 
 constexpr int kW = 4;                // warps
 constexpr int kHB = 16;              // query heads of a unit
-constexpr int kPerSM = 3;            // CTAs per SM: the step's dependent latencies need about twelve warps
+// CTAs per SM: the step's dependent latencies need about twelve warps.  That leaves 168 registers a thread, of which the
+// FP8 kernel for dh 128 spills 12 to 24 bytes.
+constexpr int kPerSM = 3;
 constexpr int kRingBytes = 70 * 1024;
 
 // CT: tokens per chunk.  FP8 chunks are 32 where the pages allow it: a step's instructions that do not grow with the

@@ -6,8 +6,10 @@
 // 4 tx + 32 j of the output rows.  A warp is then 4 rows x 8 columns, whose 16-byte reads touch each bank once, and RM =
 // RN = 4 make 64 FMAs of eight reads.  Up to dh 64 a block has two groups, which take every other tile of keys and are
 // joined at the end: a short window over a few thousand tokens has too few blocks to hide the reads' latency otherwise
-// (2048 tokens, 8 heads of 64, window 128: 45.4 us, 48.8 with one group).  Bound by issue of FMAs between reads (4096 tokens, 16 heads
-// of 128, window 1000: 932 us, 42% of the FP32 rate; 1143 as 256 threads of 16 x 16 with 32 FMAs of six reads).
+// (2048 tokens, 8 heads of 64, window 128: 45.4 us, 48.8 with one group).  Bound by issue of FMAs between reads (4096
+// tokens, 16 heads over 4 of 128, window 1000: 912 us, 43% of the FP32 rate; 1143 as 256 threads of 16 x 16 with 32 FMAs of
+// six reads).  bf16 with the head dims that come here, causal 4096 tokens, 16 heads over 4: 2.45 ms at dh 72, 5.0 ms at
+// dh 256.  fp32 above dh 128 spills registers (268 bytes up to dh 256, 204 up to 512), as no smaller tile was tried there.
 #include "sliding.cuh"
 
 namespace hcsa {
