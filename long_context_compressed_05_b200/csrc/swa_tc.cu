@@ -377,6 +377,64 @@ __device__ __forceinline__ void attend_rows(const Args &p, const Unit &x, int s,
     }
 }
 
+template <int DH>
+__device__ __forceinline__ __nv_bfloat16 *out_row(const Args &p, const Unit &x, int s, int row) {
+    const int tl = row / p.G;
+    return (__nv_bfloat16 *)p.a.out + (x.first(s, p.tb) + tl) * p.a.ld_out + (int64_t)(x.g * p.G + row - tl * p.G) * DH;
+}
+// Rows (of the 32 from r0 of sub-tile s, those in `rows`, tokens ta .. te) of which a channel is finite, so that their weights
+// are, and whose other channels each have an infinite or NaN value that the row sees: the class of those values is all that
+// there is to set, and a pass over the values finds it.  Returns the rows set.
+template <int DH>
+__device__ __forceinline__ uint32_t class_rows(const Args &p, const Unit &x, int s, int r0, uint32_t rows, int ta, int te, int lane) {
+    constexpr int NW = DH / 64;      // words of a lane: channels 2 NW lane ..
+    const SwaArgs &a = p.a;
+    struct Class {                   // a bit per half-word (15 and 31): infinite values by sign, NaN both
+        uint32_t up[NW], down[NW];
+    };
+    auto see = [&](int64_t j, Class &c) {
+        const uint32_t *v = reinterpret_cast<const uint32_t *>((const __nv_bfloat16 *)a.v + j * a.ld_v + x.g * DH) + NW * lane;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const uint32_t r = __ldg(v + w), b = bad_halves(r);
+            if (!b) continue;
+            const uint32_t nan = (((r & 0x007F007Fu) + 0x007F007Fu) & 0x00800080u) << 8 & b;   // a mantissa bit
+            c.up[w] |= (b & ~r) | nan;
+            c.down[w] |= (b & r) | nan;
+        }
+    };
+    Class core{};                    // of the tokens that all of ta .. te see
+#pragma unroll 8
+    for (int j = 0; j < a.sinks && j <= ta && j <= te - a.window; ++j) see(j, core);
+#pragma unroll 8
+    for (int j = te - a.window + 1 > 0 ? te - a.window + 1 : 0; j <= ta; ++j) see(j, core);
+    uint32_t done = 0;
+    for (uint32_t left = rows; left; left &= left - 1) {
+        const int i = __ffs(left) - 1, t = x.first(s, p.tb) + (r0 + i) / p.G;
+        Class c = core;
+        for (int j = t - a.window + 1 > 0 ? t - a.window + 1 : 0; j <= ta && j <= te - a.window; ++j) see(j, c);
+        for (int j = ta + 1; j <= t; ++j)
+            if (j > t - a.window || j < a.sinks) see(j, c);
+        uint32_t *o = reinterpret_cast<uint32_t *>(out_row<DH>(p, x, s, r0 + i)) + NW * lane;
+        uint32_t bad[NW];
+        bool open = false;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            bad[w] = bad_halves(o[w]);
+            open = open || (bad[w] & ~(c.up[w] | c.down[w]));
+        }
+        if (__any_sync(0xffffffffu, open)) continue;
+        done |= 1u << i;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const uint32_t both = c.up[w] & c.down[w] & bad[w], all = (bad[w] >> 15) * 0xFFFFu;
+            // infinity 7F80, with its sign; NaN: a mantissa bit more
+            if (bad[w]) o[w] = (o[w] & ~all) | (all & 0x7F807F80u) | (bad[w] & c.down[w] & ~both) | both >> 9;
+        }
+    }
+    return done;
+}
+
 // Is a value of key head g in tokens [lo, hi) infinite or NaN?
 template <int DH>
 __device__ bool values_bad(const SwaArgs &a, int g, int64_t lo, int64_t hi, int lane) {
@@ -398,21 +456,27 @@ __device__ __noinline__ void redo_rows(const Args &p, int s, int quad, int lane)
         const int u = nth_unit(p, k);
         if (u < 0) break;
         const Unit x = unit_of(p, u);
-        uint32_t bad = 0;
-        for (int i = 0; i < 32; ++i) {
-            const int r = 32 * quad + i, tl = r / p.G, t = x.first(s, p.tb) + tl, h = x.g * p.G + r - tl * p.G;
-            if (tl >= p.tb || t > x.last(s, p.tb)) break;
-            const uint32_t *o = reinterpret_cast<const uint32_t *>((const __nv_bfloat16 *)a.out + t * a.ld_out + (int64_t)h * DH);
-            uint32_t b = 0;
-            for (int d = lane; d < DH / 2; d += 32) b |= bad_halves(o[d]);
-            if (__any_sync(0xffffffffu, b)) bad |= 1u << i;
+        const int row = 32 * quad + lane, tl = row / p.G;
+        uint32_t b = 0, all = 0x80008000u;
+        if (tl < p.tb && x.first(s, p.tb) + tl <= x.last(s, p.tb)) {
+            const uint4 *o = reinterpret_cast<const uint4 *>(out_row<DH>(p, x, s, row));
+#pragma unroll
+            for (int d = 0; d < DH / 8; ++d) {
+                const uint4 r = o[d];
+                const uint32_t h[4] = {bad_halves(r.x), bad_halves(r.y), bad_halves(r.z), bad_halves(r.w)};
+                b |= h[0] | h[1] | h[2] | h[3];
+                all &= h[0] & h[1] & h[2] & h[3];
+            }
         }
+        uint32_t bad = __ballot_sync(0xffffffffu, b);
+        const uint32_t some = __ballot_sync(0xffffffffu, all != 0x80008000u);   // a channel is finite (of either half)
         if (!bad) continue;
         const int ta = x.first(s, p.tb) + (32 * quad + __ffs(bad) - 1) / p.G, te = x.first(s, p.tb) + (32 * quad + 31 - __clz(bad)) / p.G;
         const int behind = min(a.row1, x.w0 + x.c.n_tiles * kKT - x.c.pad);   // tokens loaded for the block
         if (!values_bad<DH>(a, x.g, x.w0, (int64_t)te - a.window + 1, lane) && !values_bad<DH>(a, x.g, ta + 1, behind, lane) &&
             !(x.c.pad && values_bad<DH>(a, x.g, x.c.sk, x.c.pad, lane)))
             continue;
+        if (bad & some) bad &= ~class_rows<DH>(p, x, s, 32 * quad, bad & some, ta, te, lane);
         for (int half = 0; half < 2; ++half)
             if (bad >> (16 * half) & 0xFFFFu) attend_rows<DH>(p, x, s, 32 * quad + 16 * half, bad >> (16 * half) & 0xFFFFu, lane);
     }

@@ -927,3 +927,31 @@ def test_decode_fp8_nan_and_infinity_in_one_channel(h, dh):
     got = c.decode().view(4, dh)
     assert torch.isnan(got[:, 5]).all() and torch.isnan(got[:, 40]).all()
     assert torch.isfinite(got[:, :5]).all() and torch.isfinite(got[:, 6:40]).all() and torch.isfinite(got[:, 41:]).all()
+
+
+@pytest.mark.parametrize("dtype,H,Hkv,dh,window,sinks", [("bf16", 8, 2, 128, NO_WINDOW, 0), ("bf16", 4, 4, 64, 700, 300), ("bf16", 7, 1, 64, 20, 9),
+                                                         ("bf16", 1, 1, 128, 3, 0), ("f32", 4, 2, 64, NO_WINDOW, 0), ("bf16", 2, 1, 72, 90, 3)])
+def test_attend_a_channel_of_infinities(h, dtype, H, Hkv, dh, window, sinks):
+    """A channel infinite in every value is infinite in every output, another one of both signs NaN from where a row sees both; the other
+    channels are as without them."""
+    T = 3001
+    g = gen(141)
+    q, k, v = (randn(g, T, n * dh, dtype=dt(dtype)) for n in (H, Hkv, Hkv))
+    vv = v.view(T, Hkv, dh)
+    clean = vv.clone()
+    vv[:, :, 5], vv[:, :, 30], vv[1500, :, 30] = math.inf, -math.inf, math.inf
+    vv[2000, 0, 11] = math.nan
+    out = torch.empty_like(q)
+    h.swa_attend(attend_params(h, T, H, Hkv, dh, window, sinks, dtype), q, k, v, out)
+    got = out.view(T, H, dh)
+    mask = seen_mask(torch.arange(T, device="cuda"), T, window, sinks)
+    assert (got[:, :, 5] == math.inf).all()
+    both = mask[:, 1500] & (mask.sum(1) > 1)
+    assert torch.isnan(got[both][:, :, 30]).all() and (got[~mask[:, 1500]][:, :, 30] == -math.inf).all()
+    head = torch.arange(H, device="cuda") < H // Hkv
+    assert torch.equal(torch.isnan(got[:, :, 11]), mask[:, 2000, None] & head)
+    clean[:, :, [5, 30]] = 0
+    got[:, :, [5, 30]] = 0
+    clean[2000, 0, 11] = 0
+    plain, _, _ = attend64(q.view(T, H, dh), k.view(T, Hkv, dh), clean, mask, dh ** -0.5)
+    check(torch.where(torch.isnan(got), plain, got.double()), q.view(T, H, dh), k.view(T, Hkv, dh), clean, mask, dh ** -0.5, dtype)
