@@ -13,7 +13,9 @@
 namespace hcsa {
 
 constexpr int kDirectTokens = 256;
-constexpr int kMinShare = 8;        // chunks of a piece at least (128 tokens, 256 of FP8 pages of 32 k tokens)
+// Chunks of a piece at least, so that a step over short sequences does not join more partials than it saves: 128 tokens, or
+// 256 where FP8 chunks are 32 (taken at 16-token chunks, not measured again for 32).
+constexpr int kMinShare = 8;
 
 struct Split {
     int units_per_seq;              // key heads x head blocks

@@ -14,15 +14,15 @@
 // blocks longest first, in a snake order over the CTAs.  Warps: 0 and 3 TMA, 1 and 2 MMA, 4..7 and 8..11 softmax and
 // output of sub-tile 0 and 1.
 //
-// Per tile of 128 x 128 at dh 128 the products take 1024 cycles of the tensor core and the exponentials 1024 of
-// the special-function unit: two equal bounds for a long window.  What holds it above them is the chain of a
-// sub-tile (S, softmax, P V, next S), of which TMEM has room for two.  Measured at 8192 tokens, 32 heads over 8, dh 128,
-// causal: 406 to 418 us (1340 TFLOP/s), captured.  What was tried there, beside 409: P in one part 462; parts of 64 + 64 462, four of 32 479; two
-// threads per row 466; two S buffers of 64 columns 458 (the narrow products are bound by shared memory); a quarter of
-// the exponentials by a polynomial on the FMA pipe 441; one issuing warp for both sub-tiles 497.  A window of 128 (65536
-// tokens, 64 heads over 8, dh 128: 690 us) is bound by the same chain: two tiles a block, then the output.  These are at
-// 1965 MHz; seconds of such calls run at the power limit, 1500 to 1660 MHz (480 and 820 us).  dh 64, 8192 tokens, 32 heads
-// over 8, causal: 349 us (788 TFLOP/s), by the exponentials: half the products for as many of them.
+// Per tile of 128 x 128 at dh 128 the products take 1024 cycles of the tensor core and the exponentials 1024 of the
+// special-function unit: two equal bounds for a long window.  What holds it above them is the chain of a sub-tile (S,
+// softmax, P V, next S), of which TMEM has room for two.  Measured at 8192 tokens, 32 heads over 8, dh 128, causal: 406 to
+// 418 us (1340 TFLOP/s), captured.  What was tried there, beside 409: P in one part 462; parts of 64 + 64 462, four of 32
+// 479; two threads per row 466; two S buffers of 64 columns 458 (the narrow products are bound by shared memory); a
+// quarter of the exponentials by a polynomial on the FMA pipe 441; one issuing warp for both sub-tiles 497.  A window of
+// 128 (65536 tokens, 64 heads over 8, dh 128: 690 us) is bound by the same chain: two tiles a block, then the output.
+// These are at 1965 MHz; seconds of such calls run at the power limit, 1500 to 1660 MHz (480 and 820 us).  dh 64, 8192
+// tokens, 32 heads over 8, causal: 349 us (788 TFLOP/s), by the exponentials: half the products for as many of them.
 #include "sliding.cuh"
 #include "tc_common.cuh"
 
